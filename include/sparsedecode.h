@@ -81,10 +81,16 @@ enum {
     SD_ERR_ORDER = 7          /* device: an idx row is not strictly ascending */
 };
 
-enum { SD_OP_TOPK = 1, SD_OP_SPARSE = 2, SD_OP_DENSE = 3, SD_OP_QUEST = 4 };
+enum {
+    SD_OP_TOPK = 1,
+    SD_OP_SPARSE = 2,
+    SD_OP_DENSE = 3,
+    SD_OP_QUEST = 4,
+    SD_OP_CHUNK = 5,         /* sd_chunk_attention (k_max and total_rows do not matter) */
+    SD_OP_CACHE_SPARSE = 6   /* sd_cache_sparse_decode */
+};
 
-/* Bytes of workspace that operation `op` (SD_OP_TOPK, SD_OP_SPARSE, SD_OP_DENSE, SD_OP_QUEST) needs
- * for `shape` (independent of the data and of the
+/* Bytes of workspace that operation `op` (one of SD_OP_...) needs for `shape` (independent of the data and of the
  * device).  Returns SD_ERR_INVALID_ARG / SD_ERR_UNSUPPORTED for a shape the library rejects. */
 SD_API sd_status sd_workspace_size(const sd_shape* shape, int32_t op, size_t* bytes);
 
@@ -251,6 +257,89 @@ SD_API sd_status sd_quest_append_kv(const sd_shape* shape, void* K, void* V, con
 SD_API sd_status sd_quest_index(const sd_shape* shape, const void* q, const void* boxes, const int32_t* page_table,
                                 const int32_t* lens, const int32_t* k, int32_t* idx, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* A paged cache in one of three forms, for the entry points below.  The struct is read during the call
+ * only; the memory belongs to the caller.
+ *   SD_CACHE_BF16    K, V bf16 [num_pages][P][Hkv][d]: the cache of every entry point above; scales is
+ *                    ignored.
+ *   SD_CACHE_MXFP8   K, V e4m3 bytes [num_pages][P][Hkv][d], 16-byte aligned, in the OCP microscaling
+ *                    form: blocks of 32 values along d share a power-of-two scale 2^e, stored as the byte
+ *                    e + 127.  e is the least integer in [-124, 119] with amax <= 448 * 2^e (elements saturate at
+ *                    448 where there is none: magnitudes near bf16's largest).
+ *   SD_CACHE_MXINT8  the same with int8 elements -127 .. 127: value = element * 2^e, stored as the byte
+ *                    e + 133; e is the least integer in [-133, 121] for which amax * 2^-e rounds to at
+ *                    most 127 (elements saturate at 127 where there is none).
+ *   scales           uint8 [num_pages][Hkv][P][2][4], 16-byte aligned: for each row the bytes of K's four
+ *                    blocks, then of V's.  Byte 255 marks a block that held an infinity or a NaN; its
+ *                    elements are 0 and it reads as NaN.
+ *   An 8-bit cache holds what sd_cache_write stores (no other element codes); every stored value is exact
+ *   in bf16.  A row of one KV head takes 264 bytes for K and V instead of 512. */
+enum { SD_CACHE_BF16 = 0, SD_CACHE_MXFP8 = 1, SD_CACHE_MXINT8 = 2 };
+typedef struct sd_cache {
+    int32_t format;   /* SD_CACHE_... */
+    int32_t reserved; /* 0 */
+    void* K;
+    void* V;
+    void* scales;
+} sd_cache;
+
+/* Ragged batches (sd_cache_write, sd_cache_read, sd_chunk_attention): request b owns rows
+ * row_start[b] .. row_start[b + 1] - 1 of a [total_rows] array, n_b of them (0 allowed).
+ *   row_start   int32 [B + 1], device memory: not negative, never falling, row_start[B] <= total_rows (else
+ *               SD_ERR_INVALID_ARG in dev_status and nothing is done).  Rows before row_start[0] and from
+ *               row_start[B] on belong to no request: inputs there are not used, outputs left as they were.
+ *   total_rows  rows of the arrays, 1 .. 2^31 - 1 - 2^16, with total_rows * Hq < 2^31 (else SD_ERR_UNSUPPORTED).
+ *   k_max of the shape is ignored by these three (any value >= 1).
+ *
+ * sd_cache_write puts each request's new K/V rows into the cache, rounded to its format (to nearest, ties
+ * to even).  lens[b] is the length INCLUDING the new rows: row j of request b goes to position
+ * lens[b] - n_b + j (n_b > lens[b]: SD_ERR_INVALID_ARG, the request's rows are not written).  lens is not
+ * changed, so the same call may be repeated.
+ *   k_new, v_new  bf16 [total_rows][Hkv][d], device memory, 16-byte aligned.
+ *   boxes         NULL, or the Quest boxes (as for sd_quest_summarize; of the values as stored) to keep
+ *                 current: the box of every page that gets a row becomes that of its rows, with the stored
+ *                 box taken in where the page held earlier rows of the request.  A block that reads as NaN
+ *                 leaves the other rows' bounds (NaN inputs are invalid to sd_quest_index).
+ * Two requests must not map new rows to the same page. */
+SD_API sd_status sd_cache_write(const sd_shape* shape, const sd_cache* cache, const int32_t* page_table,
+                                const int32_t* lens, const int32_t* row_start, int32_t total_rows, const void* k_new,
+                                const void* v_new, void* boxes, int32_t* dev_status, void* stream);
+
+/* sd_cache_read copies positions first[b] .. first[b] + n_b - 1 of every request out as contiguous bf16 rows
+ * (exactly the stored values).
+ *   first         int32 [B], device memory; 0 <= first[b] and first[b] + n_b <= lens[b] (else
+ *                 SD_ERR_INVALID_ARG and the request's rows are left as they were).
+ *   k_out, v_out  bf16 [total_rows][Hkv][d], device memory, 16-byte aligned; one of them may be NULL.  With
+ *                 row_start[b] a multiple of 16 the result is itself a bf16 cache whose pages lie in order. */
+SD_API sd_status sd_cache_read(const sd_shape* shape, const sd_cache* cache, const int32_t* page_table,
+                               const int32_t* lens, const int32_t* first, const int32_t* row_start, int32_t total_rows,
+                               void* k_out, void* v_out, int32_t* dev_status, void* stream);
+
+/* Causal attention of each request's newest n_b positions -- a prompt, a chunk of one, a drafted run of
+ * tokens to verify, or one token -- over everything its cache holds.  lens[b] includes the chunk, whose K/V
+ * rows are in the cache already (sd_cache_write); row j of request b is position p = lens[b] - n_b + j:
+ *   out[row, h] = sum_{i <= p} w_i V[b, h/G, i],  w = softmax over 0 <= i <= p of
+ *   (q[row, h] . K[b, h/G, i]) / sqrt(d).
+ *   q    bf16 [total_rows][Hq][d], device memory, 16-byte aligned.
+ *   out  bf16 [total_rows][Hq][d], device memory, 16-byte aligned: rounded once, from fp32 sums.  The
+ *        probabilities enter the second product as bf16 (their sum is taken before that, in fp32).
+ *   n_b > lens[b]: SD_ERR_INVALID_ARG and the request's rows are left as they were.  K and V of the positions
+ *   below lens[b] must be finite (a position that a row may not see counts with weight 0, and 0 * inf is NaN);
+ *   what the pages hold behind lens[b] does not matter.
+ *   workspace  sd_workspace_size(shape, SD_OP_CHUNK). */
+SD_API sd_status sd_chunk_attention(const sd_shape* shape, const sd_cache* cache, const void* q,
+                                    const int32_t* page_table, const int32_t* lens, const int32_t* row_start,
+                                    int32_t total_rows, void* out, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/* sd_sparse_decode over an 8-bit cache: the same selection format, checks, limits and fp32 result, over the
+ * values the cache holds (SD_CACHE_BF16: SD_ERR_UNSUPPORTED, use sd_sparse_decode).  The Quest indexer reads
+ * only boxes, so sd_cache_write with boxes, sd_quest_index and this call make a decode step without any bf16
+ * cache.
+ *   workspace  sd_workspace_size(shape, SD_OP_CACHE_SPARSE). */
+SD_API sd_status sd_cache_sparse_decode(const sd_shape* shape, const sd_cache* cache, const void* q,
+                                        const int32_t* page_table, const int32_t* lens, const int32_t* idx, float* out,
+                                        void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* Self-test of failure detection (no counterpart in the pages): launches one warp that waits, with
  * the bounded-wait helper every pipeline wait of the library uses, on a barrier that nothing completes.

@@ -28,12 +28,19 @@ SD_OP_TOPK = 1
 SD_OP_SPARSE = 2
 SD_OP_DENSE = 3
 SD_OP_QUEST = 4
+SD_OP_CHUNK = 5
+SD_OP_CACHE_SPARSE = 6
+
+SD_CACHE_BF16 = 0
+SD_CACHE_MXFP8 = 1
+SD_CACHE_MXINT8 = 2
 
 SD_SAMPLED_FLAG = 1 << 30   # idx entry of a row drawn by sd_stochastic_index (position in the low 30 bits)
 
 EXPORTED = ("sd_workspace_size", "sd_topk_index", "sd_topk_scores", "sd_topk_select", "sd_topk_index_static",
             "sd_sparse_decode", "sd_stochastic_index", "sd_sparse_decode_sampled", "sd_dense_decode", "sd_append_kv",
-            "sd_quest_summarize", "sd_quest_append_kv", "sd_quest_index", "sd_selftest_wait_timeout", "sd_status_string",
+            "sd_quest_summarize", "sd_quest_append_kv", "sd_quest_index", "sd_cache_write", "sd_cache_read", "sd_chunk_attention",
+            "sd_cache_sparse_decode", "sd_selftest_wait_timeout", "sd_status_string",
             "sd_last_cuda_error", "sd_version")
 
 
@@ -41,6 +48,11 @@ class SdShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages_per_req", ctypes.c_int32),
                 ("k_max", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
+class SdCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_int32), ("K", ctypes.c_void_p),
+                ("V", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class SdError(RuntimeError):
@@ -82,11 +94,17 @@ def load():
     lib.sd_quest_append_kv.argtypes = [SH, P, P, P, P, P, P, P, I32, P, P, P]
     lib.sd_quest_summarize.argtypes = [SH, P, P, P, P, I32, P, P]
     lib.sd_quest_index.argtypes = [SH, P, P, P, P, P, P, P, SZ, P, P]
+    CH = ctypes.POINTER(SdCache)
+    lib.sd_cache_write.argtypes = [SH, CH, P, P, P, I32, P, P, P, P, P]
+    lib.sd_cache_read.argtypes = [SH, CH, P, P, P, P, I32, P, P, P, P]
+    lib.sd_chunk_attention.argtypes = [SH, CH, P, P, P, P, I32, P, P, SZ, P, P]
+    lib.sd_cache_sparse_decode.argtypes = [SH, CH, P, P, P, P, P, P, SZ, P, P]
     lib.sd_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P, P]
     lib.sd_selftest_wait_timeout.restype = I32
     for f in (lib.sd_workspace_size, lib.sd_topk_index, lib.sd_topk_scores, lib.sd_topk_select, lib.sd_sparse_decode,
               lib.sd_sparse_decode_sampled, lib.sd_stochastic_index, lib.sd_dense_decode, lib.sd_append_kv,
-              lib.sd_quest_summarize, lib.sd_quest_append_kv, lib.sd_quest_index):
+              lib.sd_quest_summarize, lib.sd_quest_append_kv, lib.sd_quest_index, lib.sd_cache_write, lib.sd_cache_read,
+              lib.sd_chunk_attention, lib.sd_cache_sparse_decode):
         f.restype = I32
     lib.sd_status_string.argtypes = [I32]
     lib.sd_status_string.restype = ctypes.c_char_p
@@ -250,6 +268,60 @@ def sd_quest_append_kv(shape, K, V, page_table, lens, k_new, v_new, k_sel, ratio
                                    _ptr(v_new), _ptr(k_sel), int(ratio), _ptr(boxes), _ptr(dev_status),
                                    _stream(stream))
     return _check(st, "sd_quest_append_kv", check)
+
+
+_CACHE_DTYPE = {SD_CACHE_BF16: torch.bfloat16, SD_CACHE_MXFP8: torch.float8_e4m3fn, SD_CACHE_MXINT8: torch.int8}
+
+
+def make_cache(fmt: int, K, V, scales=None) -> SdCache:
+    """Handle of a paged cache: K, V [num_pages][P][Hkv][d] of the format's element type and, for the 8-bit
+    formats, scales uint8 [num_pages][Hkv][P][2][4].  It keeps the tensors alive."""
+    addr = [None if t is None else t.data_ptr() for t in (K, V, scales)]
+    c = SdCache(int(fmt), 0, *addr)
+    c.tensors = (K, V, scales)
+    return c
+
+
+def empty_cache(shape: SdShape, fmt: int, device=None) -> SdCache:
+    """A zeroed cache of the shape's pages in the given format (its tensors: `.tensors`)."""
+    dev = device or "cuda"
+    size = (shape.num_pages, shape.page_size, shape.num_kv_heads, shape.head_dim)
+    K, V = (torch.zeros(size, dtype=_CACHE_DTYPE[fmt], device=dev) for _ in range(2))
+    sc = None if fmt == SD_CACHE_BF16 else torch.zeros((shape.num_pages, shape.num_kv_heads, shape.page_size, 2, 4),
+                                                       dtype=torch.uint8, device=dev)
+    return make_cache(fmt, K, V, sc)
+
+
+def sd_cache_write(shape, cache, page_table, lens, row_start, k_new, v_new, boxes, dev_status, stream=None,
+                   check=True) -> int:
+    st = load().sd_cache_write(ctypes.byref(shape), ctypes.byref(cache), _ptr(page_table), _ptr(lens), _ptr(row_start),
+                               int(k_new.shape[0]), _ptr(k_new), _ptr(v_new), _ptr(boxes), _ptr(dev_status),
+                               _stream(stream))
+    return _check(st, "sd_cache_write", check)
+
+
+def sd_cache_read(shape, cache, page_table, lens, first, row_start, k_out, v_out, dev_status, stream=None,
+                  check=True) -> int:
+    rows = int((k_out if k_out is not None else v_out).shape[0])
+    st = load().sd_cache_read(ctypes.byref(shape), ctypes.byref(cache), _ptr(page_table), _ptr(lens), _ptr(first),
+                              _ptr(row_start), rows, _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream))
+    return _check(st, "sd_cache_read", check)
+
+
+def sd_chunk_attention(shape, cache, q, page_table, lens, row_start, out, workspace, dev_status, stream=None,
+                       check=True) -> int:
+    st = load().sd_chunk_attention(ctypes.byref(shape), ctypes.byref(cache), _ptr(q), _ptr(page_table), _ptr(lens),
+                                   _ptr(row_start), int(q.shape[0]), _ptr(out), _ptr(workspace), _ws_bytes(workspace),
+                                   _ptr(dev_status), _stream(stream))
+    return _check(st, "sd_chunk_attention", check)
+
+
+def sd_cache_sparse_decode(shape, cache, q, page_table, lens, idx, out, workspace, dev_status, stream=None,
+                           check=True) -> int:
+    st = load().sd_cache_sparse_decode(ctypes.byref(shape), ctypes.byref(cache), _ptr(q), _ptr(page_table), _ptr(lens),
+                                       _ptr(idx), _ptr(out), _ptr(workspace), _ws_bytes(workspace), _ptr(dev_status),
+                                       _stream(stream))
+    return _check(st, "sd_cache_sparse_decode", check)
 
 
 def workspace_for(shape: SdShape, op: int, device=None) -> torch.Tensor:

@@ -193,6 +193,9 @@ size_t decode_workspace(const Dims& d, bool dense) {
     return use_group_walk(d) ? union_layout(d).total : sparse_layout(d).total;
 }
 
+size_t chunk_workspace() { return 256; }
+size_t cache_sparse_workspace(const Dims&) { return 256; }
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 long d_k_max_of(const sd_shape* s) { return s ? (long)s->k_max : 0; }
@@ -310,6 +313,11 @@ sd_status sd_workspace_size(const sd_shape* shape, int32_t op, size_t* bytes) {
             return SD_OK;
         case SD_OP_DENSE: *bytes = decode_workspace(d, true); return SD_OK;
         case SD_OP_QUEST: *bytes = align256((size_t)d.B * d.Hq * d.max_pages * sizeof(float)); return SD_OK;
+        case SD_OP_CHUNK: *bytes = chunk_workspace(); return SD_OK;
+        case SD_OP_CACHE_SPARSE:
+            if (!sparse_fits(d)) return SD_ERR_UNSUPPORTED;
+            *bytes = cache_sparse_workspace(d);
+            return SD_OK;
         default: return SD_ERR_INVALID_ARG;
     }
 }
@@ -588,6 +596,173 @@ sd_status sd_quest_index(const sd_shape* shape, const void* q, const void* boxes
     st = launch_status(launch_quest_score(a, s));
     if (st != SD_OK) return st;
     return launch_status(launch_quest_select(a, s));
+}
+
+namespace {
+
+// The cache handle: a known format, its buffers present and aligned.
+sd_status check_cache(const sd_cache* c) {
+    if (c == nullptr || c->reserved != 0 || !c->K || !c->V || !aligned(c->K, 16) || !aligned(c->V, 16))
+        return SD_ERR_INVALID_ARG;
+    if (c->format != SD_CACHE_BF16 && c->format != SD_CACHE_MXFP8 && c->format != SD_CACHE_MXINT8)
+        return SD_ERR_INVALID_ARG;
+    if (c->format != SD_CACHE_BF16 && (!c->scales || !aligned(c->scales, 16))) return SD_ERR_INVALID_ARG;
+    return SD_OK;
+}
+
+// A ragged batch's arrays: every count of rows times heads is kept in 32 bits.
+sd_status check_rows(const Dims& d, const int32_t* row_start, int32_t total_rows) {
+    if (!row_start || !aligned(row_start, 4) || total_rows < 1) return SD_ERR_INVALID_ARG;
+    if ((long)total_rows * d.Hq >= (1L << 31) || total_rows > 0x7fffffff - 0x10000) return SD_ERR_UNSUPPORTED;
+    return SD_OK;
+}
+
+sd_status cache_io_args(const sd_shape* shape, const sd_cache* cache, const int32_t* page_table, const int32_t* lens,
+                        const int32_t* row_start, int32_t total_rows, int32_t* dev_status, CacheIoArgs* a) {
+    Dims d;
+    sd_status st = check_shape(shape, &d);
+    if (st != SD_OK) return st;
+    st = check_cache(cache);
+    if (st != SD_OK) return st;
+    if (!page_table || !lens || !dev_status || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(dev_status, 4))
+        return SD_ERR_INVALID_ARG;
+    st = check_rows(d, row_start, total_rows);
+    if (st != SD_OK) return st;
+    *a = CacheIoArgs{};
+    a->K = cache->K;
+    a->V = cache->V;
+    a->scales = cache->format == SD_CACHE_BF16 ? nullptr : static_cast<uint8_t*>(cache->scales);
+    a->page_table = page_table;
+    a->lens = lens;
+    a->row_start = row_start;
+    a->status = dev_status;
+    a->B = d.B;
+    a->Hkv = d.Hkv;
+    a->max_pages = d.max_pages;
+    a->num_pages = d.num_pages;
+    a->total_rows = total_rows;
+    a->n_cap = d.n_cap;
+    return SD_OK;
+}
+
+}  // namespace
+
+sd_status sd_cache_write(const sd_shape* shape, const sd_cache* cache, const int32_t* page_table, const int32_t* lens,
+                         const int32_t* row_start, int32_t total_rows, const void* k_new, const void* v_new,
+                         void* boxes, int32_t* dev_status, void* stream) {
+    CacheIoArgs a;
+    sd_status st = cache_io_args(shape, cache, page_table, lens, row_start, total_rows, dev_status, &a);
+    if (st != SD_OK) return st;
+    if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) || (boxes && !aligned(boxes, 16)))
+        return SD_ERR_INVALID_ARG;
+    DeviceInfo di;
+    st = device_info(&di);
+    if (st != SD_OK) return st;
+    a.k_in = static_cast<const __nv_bfloat16*>(k_new);
+    a.v_in = static_cast<const __nv_bfloat16*>(v_new);
+    a.boxes = static_cast<__nv_bfloat16*>(boxes);
+    a.sms = di.sms;
+    return launch_status(launch_cache_write(a, cache->format, static_cast<cudaStream_t>(stream)));
+}
+
+sd_status sd_cache_read(const sd_shape* shape, const sd_cache* cache, const int32_t* page_table, const int32_t* lens,
+                        const int32_t* first, const int32_t* row_start, int32_t total_rows, void* k_out, void* v_out,
+                        int32_t* dev_status, void* stream) {
+    CacheIoArgs a;
+    sd_status st = cache_io_args(shape, cache, page_table, lens, row_start, total_rows, dev_status, &a);
+    if (st != SD_OK) return st;
+    if (!first || !aligned(first, 4) || (!k_out && !v_out) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return SD_ERR_INVALID_ARG;
+    DeviceInfo di;
+    st = device_info(&di);
+    if (st != SD_OK) return st;
+    a.first = first;
+    a.k_out = static_cast<__nv_bfloat16*>(k_out);
+    a.v_out = static_cast<__nv_bfloat16*>(v_out);
+    a.sms = di.sms;
+    return launch_status(launch_cache_read(a, cache->format, static_cast<cudaStream_t>(stream)));
+}
+
+sd_status sd_chunk_attention(const sd_shape* shape, const sd_cache* cache, const void* q, const int32_t* page_table,
+                             const int32_t* lens, const int32_t* row_start, int32_t total_rows, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    Dims d;
+    sd_status st = check_shape(shape, &d);
+    if (st != SD_OK) return st;
+    st = check_cache(cache);
+    if (st != SD_OK) return st;
+    if (!q || !page_table || !lens || !out || !workspace || !dev_status) return SD_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(page_table, 4) ||
+        !aligned(lens, 4) || !aligned(dev_status, 4))
+        return SD_ERR_INVALID_ARG;
+    st = check_rows(d, row_start, total_rows);
+    if (st != SD_OK) return st;
+    if (workspace_bytes < chunk_workspace()) return SD_ERR_WORKSPACE;
+    DeviceInfo di;
+    st = device_info(&di);
+    if (st != SD_OK) return st;
+    ChunkArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.K = cache->K;
+    a.V = cache->V;
+    a.scales = static_cast<const uint8_t*>(cache->scales);
+    a.page_table = page_table;
+    a.lens = lens;
+    a.row_start = row_start;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.status = dev_status;
+    a.B = d.B;
+    a.Hq = d.Hq;
+    a.Hkv = d.Hkv;
+    a.G = d.G;
+    a.max_pages = d.max_pages;
+    a.num_pages = d.num_pages;
+    a.total_rows = total_rows;
+    a.sms = di.sms;
+    a.n_cap = d.n_cap;
+    a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kHeadDim));
+    return launch_status(launch_chunk_attention(a, cache->format, static_cast<cudaStream_t>(stream)));
+}
+
+sd_status sd_cache_sparse_decode(const sd_shape* shape, const sd_cache* cache, const void* q,
+                                 const int32_t* page_table, const int32_t* lens, const int32_t* idx, float* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    Dims d;
+    sd_status st = check_shape(shape, &d);
+    if (st != SD_OK) return st;
+    st = check_cache(cache);
+    if (st != SD_OK) return st;
+    if (cache->format == SD_CACHE_BF16) return SD_ERR_UNSUPPORTED;
+    if (!q || !page_table || !lens || !idx || !out || !workspace || !dev_status) return SD_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(page_table, 4) ||
+        !aligned(lens, 4) || !aligned(idx, 4) || !aligned(dev_status, 4))
+        return SD_ERR_INVALID_ARG;
+    if (!sparse_fits(d)) return SD_ERR_UNSUPPORTED;
+    if (workspace_bytes < cache_sparse_workspace(d)) return SD_ERR_WORKSPACE;
+    DeviceInfo di;
+    st = device_info(&di);
+    if (st != SD_OK) return st;
+    CacheSparseArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.K = cache->K;
+    a.V = cache->V;
+    a.scales = static_cast<const uint8_t*>(cache->scales);
+    a.page_table = page_table;
+    a.lens = lens;
+    a.idx = idx;
+    a.out = out;
+    a.status = dev_status;
+    a.B = d.B;
+    a.Hq = d.Hq;
+    a.Hkv = d.Hkv;
+    a.G = d.G;
+    a.max_pages = d.max_pages;
+    a.num_pages = d.num_pages;
+    a.k_max = d.k_max;
+    a.sms = di.sms;
+    a.n_cap = d.n_cap;
+    a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kHeadDim));
+    return launch_status(launch_cache_sparse(a, cache->format, static_cast<cudaStream_t>(stream)));
 }
 
 const char* sd_status_string(sd_status status) {

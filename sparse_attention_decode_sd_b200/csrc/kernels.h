@@ -152,4 +152,59 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 
+// Ragged rows into a cache of any format and back (cache_io.cu).
+struct CacheIoArgs {
+    void* K;
+    void* V;
+    uint8_t* scales;          // 8-bit formats: [num_pages][Hkv][16][2][4], else null
+    const int32_t* page_table;
+    const int32_t* lens;
+    const int32_t* first;     // read: first position of each request
+    const int32_t* row_start; // [B + 1]
+    const __nv_bfloat16* k_in;
+    const __nv_bfloat16* v_in;
+    __nv_bfloat16* k_out;     // read: either may be null
+    __nv_bfloat16* v_out;
+    __nv_bfloat16* boxes;     // write: Quest boxes of the written pages, or null
+    int32_t* status;
+    int B, Hkv, max_pages, num_pages, total_rows, sms;
+    long n_cap;
+};
+cudaError_t launch_cache_write(const CacheIoArgs& a, int format, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheIoArgs& a, int format, cudaStream_t stream);
+
+// Attention of a chunk of new positions over a cache of any format (chunk_attention.cu).
+struct ChunkArgs {
+    const __nv_bfloat16* q;   // [total_rows][Hq][128]
+    const void* K;
+    const void* V;
+    const uint8_t* scales;
+    const int32_t* page_table;
+    const int32_t* lens;
+    const int32_t* row_start;
+    __nv_bfloat16* out;       // [total_rows][Hq][128]
+    int32_t* status;
+    int B, Hq, Hkv, G, max_pages, num_pages, total_rows, sms;
+    long n_cap;
+    float scale_log2;         // log2(e) / sqrt(d)
+};
+cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream);
+
+// Sparse decode over an 8-bit cache (cache_sparse.cu).
+struct CacheSparseArgs {
+    const __nv_bfloat16* q;
+    const void* K;
+    const void* V;
+    const uint8_t* scales;
+    const int32_t* page_table;
+    const int32_t* lens;
+    const int32_t* idx;
+    float* out;
+    int32_t* status;
+    int B, Hq, Hkv, G, max_pages, num_pages, k_max, sms;
+    long n_cap;
+    float scale_log2;
+};
+cudaError_t launch_cache_sparse(const CacheSparseArgs& a, int format, cudaStream_t stream);
+
 }  // namespace sd

@@ -193,7 +193,7 @@ size_t decode_workspace(const Dims& d, bool dense) {
     return use_group_walk(d) ? union_layout(d).total : sparse_layout(d).total;
 }
 
-size_t chunk_workspace() { return 256; }
+size_t chunk_workspace() { return chunk_layout().total; }
 size_t cache_sparse_workspace(const Dims&) { return 256; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -721,6 +721,12 @@ sd_status sd_chunk_attention(const sd_shape* shape, const sd_cache* cache, const
     a.sms = di.sms;
     a.n_cap = d.n_cap;
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kHeadDim));
+    a.tpt = 128 / d.G;
+    const ChunkLayout L = chunk_layout();
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.part = reinterpret_cast<float*>(ws + L.part);
+    a.ml = reinterpret_cast<float2*>(ws + L.ml);
+    a.tail = ws + L.tail;
     return launch_status(launch_chunk_attention(a, cache->format, static_cast<cudaStream_t>(stream)));
 }
 

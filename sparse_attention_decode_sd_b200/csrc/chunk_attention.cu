@@ -2,88 +2,872 @@
 //
 //   out[t, h] = sum_i w_i V[b, h/G, i],  w = softmax over 0 <= i <= p of (q[t, h] . K[b, h/G, i]) / sqrt(d)
 //
-// for row t = row_start[b] + j at position p = N_b - n_b + j.  One warp takes one (row, query head): lane l
-// holds dimensions 4 l .. 4 l + 3 of q and of the output, walks the positions in order with an fp32
-// online softmax and reads each K and V row in its stored form.
+// for row t = row_start[b] + j at position p = N_b - n_b + j.
+//
+// Rows of a tile.  The G query heads of a KV head read the same K and V, so a tile of 128 rows holds
+// floor(128 / G) consecutive tokens times the G heads of one group.  Two tiles make an item (256 rows, one KV
+// head of one request); its key/value tiles of 128 positions are the units of work, and all units of the
+// batch are cut evenly over one CTA per SM (each CTA works out its share from row_start and lens, so there
+// is no planning launch).  An item cut by a CTA's border leaves its partial (max, sum, output) in the
+// workspace, and merge_chunks_kernel joins the parts in order: the same result every time.
+//
+// One CTA, warp-specialised around tensor memory (512 columns: scores of the two tiles, outputs of the two
+// tiles), with
+//   warps 0-3, 4-7   softmax of tile 0 and tile 1, one row per thread
+//   warp 8           copies: K and V page by page (one TMA box of 16 rows x 64 values per page and half, in
+//                    the 128-byte swizzle, into a ring of 32 KB stages), the two tiles of q
+//   warp 9           MMAs (one thread): S = Q K^T from shared memory, O += P V with P in tensor memory
+//   warps 12-15      8-bit caches: raw tiles (16 KB + scales) to bf16 stages, exact
+// While one tile's warps take the softmax of a unit, the tensor cores work on the other tile: per unit
+// P0 V, Q0 K', P1 V, Q1 K' (K' the next unit's keys), so both are busy in turn.  P (bf16) overwrites the first
+// half of its scores.  The running maximum only moves, and the output is only rescaled, when it would grow by more
+// than 2^8 (weights then stay below 2^8; sums and outputs are fp32, and bf16 has the same precision there).
+//
+// Items of one tile (few tokens: decode, short chunks) split their units between the two warpgroups, even and odd,
+// each with a maximum, sum and output of its own, joined at the end: the two sides stay busy in turn all the same.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "cache_format.cuh"
 #include "kernels.h"
 #include "ragged.cuh"
+#include "tcgen05.cuh"
 
 namespace sd {
 
-// Four consecutive values (dimensions 4 l .. 4 l + 3) of a cache row, as fp32.
+namespace {
+
+constexpr int kTileRows = 128;                 // rows of a query tile, positions of a key/value tile
+constexpr int kHalf = 16 * 1024;               // 128 rows of 64 bf16 values
+constexpr int kStageBytes = 2 * kHalf;         // a K or V tile in bf16
+constexpr int kRawBytes = 16 * 1024;           // the same in 8 bits
+constexpr int kScaleTile = 1024;               // scales of K and V of 128 positions
+constexpr float kRescale = 8.f;                // log2 units that the maximum may lag behind
+
 template <int kFmt>
-__device__ __forceinline__ void load4(const void* base, long row, const uint8_t* scale, int l, float (&x)[4]) {
-    uint32_t lo, hi;
-    if (kFmt == kFmtBf16) {
-        const uint2 v = reinterpret_cast<const uint2*>(base)[row * 32 + l];
-        lo = v.x;
-        hi = v.y;
-    } else {
-        decode4<kFmt>(reinterpret_cast<const uint32_t*>(base)[row * 32 + l], factor_of<kFmt>(scale[l >> 3]), lo, hi);
+struct Layout {
+    static constexpr bool k8 = kFmt != kFmtBf16;
+    static constexpr int kStages = k8 ? 3 : 5;
+    static constexpr int kRaw = k8 ? 3 : 0;
+    static constexpr int kScaleSlots = k8 ? 3 : 0;
+    static constexpr int kQ = 0;
+    static constexpr int kKv = 2 * kStageBytes;
+    static constexpr int kRawOff = kKv + kStages * kStageBytes;
+    static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
+    static constexpr int kCtl = kScaleOff + kScaleSlots * kScaleTile;
+    static constexpr int kThreads = k8 ? 512 : 384;
+};
+
+struct Control {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t kv_full[5], kv_empty[5];
+    uint64_t raw_full[3], raw_empty[3];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t done;
+    uint32_t tmem;
+    int dead;                // a wait ran out: nothing more is issued
+    int b, kvh, pair, unit;  // where this CTA's share starts
+    long long scan[16];
+    float2 post[2 * kTileRows];   // maximum and sum of the two sides of a one-tile item
+};
+
+template <int kFmt>
+constexpr int chunk_smem() {
+    return Layout<kFmt>::kCtl + (int)sizeof(Control);
+}
+static_assert(chunk_smem<kFmtBf16>() <= 227 * 1024 && chunk_smem<kFmtFp8>() <= 227 * 1024, "shared memory");
+
+// A bounded wait; once one has run out, every later one returns at once.
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0; it < kWaitLimitIters; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int*>(dead)) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) break;
     }
-    x[0] = bf16_lo(lo);
-    x[1] = bf16_hi(lo);
-    x[2] = bf16_lo(hi);
-    x[3] = bf16_hi(hi);
+    *reinterpret_cast<volatile int*>(dead) = 1;
+    report(status, SD_ERR_TIMEOUT);
+    return false;
+}
+
+// ---- the batch as units --------------------------------------------------------------------------------
+struct Request {
+    int rs, n, base;   // first row, new rows, positions before them
+};
+__device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
+    Request r;
+    r.rs = a.row_start[b];
+    r.n = a.row_start[b + 1] - r.rs;
+    const int N = a.lens[b];
+    r.base = N - r.n;
+    if (N < 0 || (long)N > a.n_cap || r.base < 0) r.n = 0;   // (reported where the shares are worked out)
+    return r;
+}
+
+// Key/value tiles of item i of a request: all positions that its last token sees.  w tokens to an item.
+__device__ __forceinline__ int item_tiles(const Request& r, int i, int w) {
+    return (r.base + min(r.n, (i + 1) * w) + kTileRows - 1) / kTileRows;
+}
+// Tiles of items 0 .. i - 1.  Over p = 128 / gcd(w, 128) items their number grows by w p / 128 each, so the
+// sum over whole periods has a closed form.
+__device__ __forceinline__ long long tiles_before(const Request& r, int i, int items, int w) {
+    const int k = min(i, items - 1);
+    const int p = kTileRows / min(kTileRows, w & -w), s = w * p / kTileRows;
+    const int whole = k / p, rest = k - whole * p;
+    long long sum = 0, first = 0;
+    if (whole > 0) {
+        for (int x = 0; x < p; ++x) first += item_tiles(r, x, w);
+        sum = whole * first + (long long)p * s * whole * (whole - 1) / 2;
+    }
+    for (int x = 0; x < rest; ++x) sum += item_tiles(r, x, w) + (long long)whole * s;
+    if (i == items) sum += item_tiles(r, items - 1, w);
+    return sum;
+}
+
+// One stretch of consecutive units of one item.
+struct Segment {
+    int b, kvh;
+    int rows;     // first row (token) of the item in q and out
+    int tokens;   // tokens of the item
+    int first;    // position of its first token
+    int end;      // positions that its last token sees
+    int j0, j1;   // key/value tiles of the stretch
+    int tiles;    // key/value tiles of the item
+    bool two;     // the item has a second tile of rows
+};
+
+struct Walk {
+    const ChunkArgs& a;
+    int w, b, kvh, i, j, items;
+    long long left;
+    Request r;
+    __device__ Walk(const ChunkArgs& args, const Control& c, long long units)
+        : a(args), w(2 * args.tpt), b(c.b), kvh(c.kvh), i(c.pair), j(c.unit), left(units) {
+        if (left > 0) {
+            r = request(a, b);
+            items = (r.n + w - 1) / w;
+        }
+    }
+    __device__ __forceinline__ bool next(Segment& s) {
+        if (left <= 0) return false;
+        s.b = b;
+        s.kvh = kvh;
+        s.rows = r.rs + i * w;
+        s.tokens = min(w, r.n - i * w);
+        s.first = r.base + i * w;
+        s.end = s.first + s.tokens;
+        s.tiles = (s.end + kTileRows - 1) / kTileRows;
+        s.j0 = j;
+        s.j1 = (int)min((long long)s.tiles, j + left);
+        s.two = s.tokens > a.tpt;
+        left -= s.j1 - s.j0;
+        j = s.j1;
+        if (left > 0) {   // the stretch ended with its item
+            j = 0;
+            if (++i == items) {
+                i = 0;
+                if (++kvh == a.Hkv) {
+                    kvh = 0;
+                    do {
+                        r = request(a, ++b);
+                    } while (r.n == 0);
+                    items = (r.n + w - 1) / w;
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// What the merge needs of a CTA whose last item goes on in later CTAs (valid), written by every CTA.
+struct TailRecord {
+    int valid, rows, tokens, kvh, last, pad[3];
+};
+
+__device__ __forceinline__ float* slot_out(const ChunkArgs& a, int slot) {
+    return a.part + (long)slot * (2 * kTileRows) * kHeadDim;
+}
+__device__ __forceinline__ float2* slot_ml(const ChunkArgs& a, int slot) { return a.ml + (long)slot * (2 * kTileRows); }
+
+// CTAs that get units: each of them at least one, so that the parts of a cut item lie in neighbouring CTAs.
+__device__ __forceinline__ long long shares(long long total) { return min(total, (long long)gridDim.x); }
+
+// The block's share [u0, u1) of the batch's units, its start in `c`, and the checks of row_start and lens.
+// False where row_start is not valid (nothing is done then).
+__device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& u0, long long& u1, long long& total) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int per = (a.B + blockDim.x - 1) / blockDim.x, w = 2 * a.tpt;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    bool bad = false;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int lo = a.row_start[b], hi = a.row_start[b + 1];
+        bad = bad || lo < 0 || hi < lo || hi > a.total_rows;
+        const int N = a.lens[b];
+        if (N < 0 || (long)N > a.n_cap || (hi > lo && hi - lo > N)) {
+            if (blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
+            continue;
+        }
+        if (bad || hi == lo) continue;
+        const Request r = {lo, hi - lo, N - (hi - lo)};
+        const int items = (r.n + w - 1) / w;
+        mine += a.Hkv * tiles_before(r, items, items, w);
+    }
+    if (__syncthreads_or(bad ? 1 : 0)) {
+        if (tid == 0 && blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
+        total = u0 = u1 = 0;
+        return false;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) c.scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    total = 0;
+    for (int x = 0; x < warps; ++x) {
+        if (x < warp) before += c.scan[x];
+        total += c.scan[x];
+    }
+    const long long parts = shares(total);
+    u0 = min((long long)blockIdx.x, parts) * total / max(parts, 1ll);
+    u1 = min((long long)blockIdx.x + 1, parts) * total / max(parts, 1ll);
+    if (u1 > u0 && before <= u0 && u0 < before + mine) {   // the share starts in this thread's requests
+        long long at = u0 - before;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request(a, b);
+            if (r.n == 0) continue;
+            const int items = (r.n + w - 1) / w;
+            const long long head = tiles_before(r, items, items, w);
+            if (at >= head * a.Hkv) {
+                at -= head * a.Hkv;
+                continue;
+            }
+            c.b = b;
+            c.kvh = (int)(at / head);
+            at -= c.kvh * head;
+            int lo = 0, hi = items - 1;   // the last item with tiles_before <= at
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (tiles_before(r, mid, items, w) <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            c.pair = lo;
+            c.unit = (int)(at - tiles_before(r, lo, items, w));
+            break;
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
+// ---- warp 8: copies -------------------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(128) chunk_attention_kernel(ChunkArgs a) {
-    extern __shared__ int row_starts[];
-    pdl_enter();
-    if (!load_row_start(a.row_start, a.B, a.total_rows, row_starts, a.status)) return;
-    const int l = threadIdx.x & 31;
-    const long unit = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = (int)(unit % a.Hq);
-    const long t = unit / a.Hq;
-    if (t >= a.total_rows) return;
-    if (t < row_starts[0] || t >= row_starts[a.B]) return;
-    const int b = request_of(row_starts, a.B, (int)t), rs = row_starts[b], re = row_starts[b + 1];
-    const int N = checked_len(a.lens, b, a.n_cap, a.status);
-    if (re - rs > N) {
-        report(a.status, SD_ERR_INVALID_ARG);
-        return;
+__device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_t* smem, Walk walk, const CUtensorMap* qm,
+                                          const CUtensorMap* km, const CUtensorMap* vm) {
+    using L = Layout<kFmt>;
+    const int lane = threadIdx.x & 31;
+    constexpr int kRing = L::k8 ? L::kRaw : L::kStages;
+    uint64_t* full = L::k8 ? c.raw_full : c.kv_full;
+    uint64_t* empty = L::k8 ? c.raw_empty : c.kv_empty;
+    const uint32_t base = smem_addr(smem);
+    const int my = L::k8 ? (lane & 7) : (lane >> 1) & 7;   // the page of the tile that this lane copies
+    uint32_t ring = 0, q_count[2] = {0, 0}, unit_count = 0;
+    Segment s;
+    while (walk.next(s)) {
+        for (int t = 0; t < (s.two ? 2 : 1); ++t) {
+            const bool ok = pipe_wait(&c.q_empty[t], (q_count[t] & 1) ^ 1, &c.dead, a.status);
+            ++q_count[t];
+            if (lane == 0 && ok) {
+                mbar_arrive_expect_tx(&c.q_full[t], (uint32_t)(a.tpt * a.G * kRowBytes));
+                for (int h = 0; h < 2; ++h)
+                    tma_load_3d(base + L::kQ + t * kStageBytes + h * kHalf, qm, h * 64, s.kvh * a.G, s.rows + t * a.tpt,
+                                &c.q_full[t]);
+            }
+            __syncwarp();
+        }
+        const int pages = (s.end + kPageSize - 1) / kPageSize, count = s.j1 - s.j0;
+        auto page_of = [&](int t) {   // -1: none there (behind the last position, or a bad entry)
+            const int pi = (s.j0 + t) * (kTileRows / kPageSize) + my;
+            if (t >= count || pi >= pages) return -1;
+            return a.page_table[(long)s.b * a.max_pages + pi];
+        };
+        auto load = [&](bool v, int t, int page) {
+            const bool there = (s.j0 + t) * (kTileRows / kPageSize) + my < pages;
+            const bool good = there && page >= 0 && page < a.num_pages;
+            if (there && !good) report(a.status, SD_ERR_INDEX_OOB);
+            const int st = ring % kRing;
+            const bool ok = pipe_wait(&empty[st], ((ring / kRing) & 1) ^ 1, &c.dead, a.status);
+            ++ring;
+            if (!__all_sync(0xffffffffu, ok)) return;
+            uint32_t bytes;
+            bool copies;
+            if (L::k8) {   // lanes 0-7: elements; lanes 8-15: the scales of both, with K
+                copies = good && (lane < 8 || (lane < 16 && !v));
+                bytes = __popc(__ballot_sync(0xffffffffu, copies && lane < 8)) * (kPageSize * kHeadDim) +
+                        __popc(__ballot_sync(0xffffffffu, copies && lane >= 8)) * (kPageSize * 2 * kScaleBytes);
+            } else {
+                copies = good && lane < 16;
+                bytes = __popc(__ballot_sync(0xffffffffu, copies)) * (kPageSize * kRowBytes / 2);
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+            __syncwarp();
+            if (copies) {
+                const CUtensorMap* m = v ? vm : km;
+                if (L::k8) {
+                    if (lane < 8)
+                        tma_load_3d(base + L::kRawOff + st * kRawBytes + my * (kPageSize * kHeadDim), m, 0, s.kvh,
+                                    page * kPageSize, &full[st]);
+                    else
+                        bulk_copy_g2s(smem + L::kScaleOff + (unit_count % 3) * kScaleTile + my * (kPageSize * 2 * kScaleBytes),
+                                      a.scales + scale_offset(page, s.kvh, 0, a.Hkv), kPageSize * 2 * kScaleBytes, &full[st]);
+                } else {
+                    const int h = lane & 1;
+                    tma_load_3d(base + L::kKv + st * kStageBytes + h * kHalf + my * (kPageSize * 128), m, h * 64, s.kvh,
+                                page * kPageSize, &full[st]);
+                }
+            }
+            if (!v) ++unit_count;
+            __syncwarp();
+        };
+        const int ahead = s.two ? 1 : 2;   // key tiles before the first value tile, as the MMAs take them
+        int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2), p3 = page_of(3);
+        load(false, 0, p0);
+        if (ahead == 2 && count > 1) load(false, 1, p1);
+        for (int t = 0; t < count; ++t) {
+            load(true, t, p0);
+            if (t + ahead < count) load(false, t + ahead, ahead == 1 ? p1 : p2);
+            p0 = p1;
+            p1 = p2;
+            p2 = p3;
+            p3 = page_of(t + 4);
+        }
     }
-    const int seen = N - (re - rs) + (int)(t - rs) + 1, kvh = h / a.G;
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, sum = 0.f;
-    load4<kFmtBf16>(a.q, t * a.Hq + h, nullptr, l, q);
-    int page = 0;
-    for (int p = 0; p < seen; ++p) {
-        if (p % kPageSize == 0) {
-            page = a.page_table[(long)b * a.max_pages + p / kPageSize];
-            if (page < 0 || page >= a.num_pages) {
-                report(a.status, SD_ERR_INDEX_OOB);
-                return;
+    // every copy has landed before the block ends (also after a wait that ran out)
+    for (uint32_t x = ring > (uint32_t)kRing ? ring - kRing : 0; x < ring; ++x)
+        if (!c.dead) mbar_wait(&full[x % kRing], (x / kRing) & 1);
+    if (c.dead) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+    }
+}
+
+// ---- warp 9: MMAs -----------------------------------------------------------------------------------------
+template <int kFmt>
+__device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t* smem, Walk walk) {
+    using L = Layout<kFmt>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(smem), tm = c.tmem;
+    constexpr uint32_t kQk = mma_idesc(128, 128, false), kPv = mma_idesc(128, 128, true);
+    uint32_t ring = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+    Segment s;
+
+    auto wait_stage = [&]() -> uint32_t {   // the next stage of the ring, full
+        const uint32_t st = ring % L::kStages;
+        pipe_wait(&c.kv_full[st], (ring / L::kStages) & 1, &c.dead, a.status);
+        ++ring;
+        return st;
+    };
+    auto live = [&]() { return *reinterpret_cast<volatile int*>(&c.dead) == 0; };
+    auto qk = [&](int g, int tile, uint32_t st) {
+        const uint32_t q = base + L::kQ + tile * kStageBytes, k = base + L::kKv + st * kStageBytes;
+        if (lane == 0 && live()) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t off = (x >> 2) * kHalf + (x & 3) * 32;
+                mma_ss(tm + g * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kQk, x > 0);
+            }
+            mma_commit(&c.s_full[g]);
+        }
+        __syncwarp();
+    };
+    auto pv = [&](int g, uint32_t st, bool add) {
+        const uint32_t v = base + L::kKv + st * kStageBytes;
+        pipe_wait(&c.p_full[g], p_count[g] & 1, &c.dead, a.status);
+        ++p_count[g];
+        tc_fence_after();
+        if (lane == 0 && live()) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                mma_ts(tm + 256 + g * 128, tm + g * 128 + x * 8, smem_desc(v + x * 2048, kHalf, 1024), kPv, add || x > 0);
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+        if (lane == 0 && live()) mma_commit(bar);
+        __syncwarp();
+    };
+    // The value rows behind the item's last position are zeroed: their weights are zero, and 0 * NaN is NaN.
+    auto clear_tail = [&](uint32_t st, int t) {
+        const int from = s.end - (s.j0 + t) * kTileRows;
+        if (L::k8 || from >= kTileRows) return;
+        uint8_t* v = smem + L::kKv + st * kStageBytes;
+        for (int x = from * 8 + lane; x < kTileRows * 8; x += 32) {
+            reinterpret_cast<uint4*>(v)[x] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(v + kHalf)[x] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+        __syncwarp();
+    };
+
+    while (walk.next(s)) {
+        const int count = s.j1 - s.j0;
+        pipe_wait(&c.q_full[0], q_count[0] & 1, &c.dead, a.status);
+        ++q_count[0];
+        if (s.two) {
+            pipe_wait(&c.q_full[1], q_count[1] & 1, &c.dead, a.status);
+            ++q_count[1];
+            uint32_t k = wait_stage();
+            qk(0, 0, k);
+            qk(1, 1, k);
+            commit(&c.kv_empty[k]);
+            for (int t = 0; t < count; ++t) {
+                const uint32_t v = wait_stage();
+                const bool more = t + 1 < count;
+                clear_tail(v, t);
+                if (more) k = wait_stage();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    pv(g, v, t > 0);
+                    if (g == 1) commit(&c.kv_empty[v]);
+                    if (more) qk(g, g, k);
+                    else commit(&c.o_full[g]);
+                }
+                if (more) commit(&c.kv_empty[k]);
+            }
+            commit(&c.q_empty[0]);
+            commit(&c.q_empty[1]);
+        } else {
+            for (int g = 0; g < 2 && g < count; ++g) {
+                const uint32_t k = wait_stage();
+                qk(g, 0, k);
+                commit(&c.kv_empty[k]);
+            }
+            for (int t = 0; t < count; ++t) {
+                const int g = t & 1;
+                const uint32_t v = wait_stage();
+                clear_tail(v, t);
+                pv(g, v, t > 1);
+                commit(&c.kv_empty[v]);
+                if (t + 2 < count) {
+                    const uint32_t k = wait_stage();
+                    qk(g, 0, k);
+                    commit(&c.kv_empty[k]);
+                } else {
+                    commit(&c.o_full[g]);
+                }
+            }
+            commit(&c.q_empty[0]);
+        }
+    }
+    if (lane == 0) mma_commit(&c.done);   // everything issued has ended before tensor memory is given back
+    __syncwarp();
+    mbar_wait(&c.done, 0);
+}
+
+// ---- warps 12-15 (8-bit caches): raw tiles to bf16 stages -------------------------------------------------
+template <int kFmt>
+__device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uint8_t* smem, Walk walk) {
+    using L = Layout<kFmt>;
+    const int tid = threadIdx.x & 127;
+    uint32_t ring = 0, unit[2] = {0, 0};
+    Segment s;
+    auto tile = [&](bool v, int t) {
+        const uint32_t raw = ring % L::kRaw, st = ring % L::kStages;
+        pipe_wait(&c.raw_full[raw], (ring / L::kRaw) & 1, &c.dead, a.status);
+        pipe_wait(&c.kv_empty[st], ((ring / L::kStages) & 1) ^ 1, &c.dead, a.status);
+        ++ring;
+        const uint8_t* src = smem + L::kRawOff + raw * kRawBytes;
+        const uint8_t* sc = smem + L::kScaleOff + (unit[v] % 3) * kScaleTile + (v ? kScaleBytes : 0);
+        ++unit[v];
+        uint8_t* dst = smem + L::kKv + st * kStageBytes;
+        const int c16 = tid & 7, h = c16 >> 2;
+        const int rows = min(kTileRows, s.end - (s.j0 + t) * kTileRows);   // rows behind them become zero
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int row = x * 16 + (tid >> 3);
+            uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+            if (row < rows) {
+                const uint4 e = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
+                const Factor f = factor_of<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
+                decode4<kFmt>(e.x, f, o[0].x, o[0].y);
+                decode4<kFmt>(e.y, f, o[0].z, o[0].w);
+                decode4<kFmt>(e.z, f, o[1].x, o[1].y);
+                decode4<kFmt>(e.w, f, o[1].z, o[1].w);
+            }
+            // lanes of the upper half write their second chunk first: eight lanes, eight bank groups
+            uint8_t* line = dst + h * kHalf + row * 128;
+            const int k0 = 2 * (c16 & 3);
+            *reinterpret_cast<uint4*>(line + (((k0 + h) ^ (row & 7)) << 4)) = h ? o[1] : o[0];
+            *reinterpret_cast<uint4*>(line + (((k0 + 1 - h) ^ (row & 7)) << 4)) = h ? o[0] : o[1];
+        }
+        fence_proxy_async();
+        mbar_arrive(&c.kv_full[st]);
+        mbar_arrive(&c.raw_empty[raw]);
+    };
+    while (walk.next(s)) {
+        const int count = s.j1 - s.j0, ahead = s.two ? 1 : 2;
+        tile(false, 0);
+        if (ahead == 2 && count > 1) tile(false, 1);
+        for (int t = 0; t < count; ++t) {
+            tile(true, t);
+            if (t + ahead < count) tile(false, t + ahead);
+        }
+    }
+}
+
+// ---- warps 0-7: softmax and output --------------------------------------------------------------------------
+__device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c, Walk walk, long long u1, long long total) {
+    const int cta = blockIdx.x;
+    const int g = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t sc = c.tmem + g * 128 + lanes, oc = c.tmem + 256 + lanes;
+    const int tq = row / a.G, gi = row - tq * a.G;
+    const float scale = a.scale_log2;
+    uint32_t s_count = 0, o_count = 0;
+    Segment s = {};
+    while (walk.next(s)) {
+        const int tile = s.two ? g : 0, step = s.two ? 1 : 2, count = s.j1 - s.j0;
+        const int token = tile * a.tpt + tq;
+        const bool valid = tq < a.tpt && token < s.tokens;
+        const int lim = valid ? s.first + token : s.end - 1;   // last position that the row sees
+        const int lowest = s.first + tile * a.tpt;             // least of these in the tile
+        float m = -INFINITY, l = 0.f;
+        bool begun = false;
+        for (int t = s.two ? 0 : g; t < count; t += step) {
+            bool ok = pipe_wait(&c.s_full[g], s_count & 1, &c.dead, a.status);
+            ++s_count;
+            if (!__all_sync(0xffffffffu, ok)) continue;
+            tc_fence_after();
+            uint32_t r[4][32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld32(sc + x * 32, r[x]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_loaded(r[x]);
+            const int col0 = (s.j0 + t) * kTileRows;
+            if (col0 + kTileRows - 1 > lowest) {
+                const int last = lim - col0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (x * 32 + y > last) r[x][y] = 0xff800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 32; y += 2)
+                    mx[x] = max3(mx[x], __uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool grow = (top - m) * scale > kRescale;   // (from -infinity: any finite score)
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? ex2((m - top) * scale) : 1.f;
+                if (grow) m = top;
+                l *= f;
+                if (begun) {
+                    const uint64_t f2 = pair_of(f, f);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(oc + g * 128 + x * 32, o);
+                        tmem_wait_ld();
+                        tmem_loaded(o);
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) {
+                            float lo, hi;
+                            split_pair(mul2(pair_of(__uint_as_float(o[y]), __uint_as_float(o[y + 1])), f2), lo, hi);
+                            o[y] = __float_as_uint(lo);
+                            o[y + 1] = __float_as_uint(hi);
+                        }
+                        tmem_st32(oc + g * 128 + x * 32, o);
+                    }
+                }
+            }
+            begun = true;
+            const float shift = m == -INFINITY ? 0.f : -m * scale;
+            const uint64_t sc2 = pair_of(scale, scale), sh2 = pair_of(shift, shift);
+            uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t p[32];
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                    const uint32_t(&src)[32] = r[x * 2 + (y >> 4)];
+                    const int z = (y & 15) * 2;
+                    float lo, hi;
+                    split_pair(fma2(pair_of(__uint_as_float(src[z]), __uint_as_float(src[z + 1])), sc2, sh2), lo, hi);
+                    lo = ex2(lo);
+                    hi = ex2(hi);
+                    sum[y & 1] = add2(sum[y & 1], pair_of(lo, hi));
+                    p[y] = pack_bf16x2(lo, hi);
+                }
+                tmem_st32(sc + x * 32, p);
+            }
+            float s0, s1;
+            split_pair(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&c.p_full[g]);
+        }
+        // the stretch's output: final rows, or a part for the merge
+        const bool mine = s.two || g < count;
+        if (mine) {
+            pipe_wait(&c.o_full[g], o_count & 1, &c.dead, a.status);
+            ++o_count;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const bool whole = s.j0 == 0 && s.j1 == s.tiles;
+        const int slot = 2 * cta + (s.j0 > 0 ? 0 : 1);
+        float f0 = 1.f, f1 = 0.f;   // weights of the two sides' outputs
+        int from = 0, to = 4;       // 32-column blocks that this thread writes
+        bool both = false;
+        if (!s.two) {
+            c.post[g * kTileRows + row] = make_float2(m, l);
+            tc_fence_before();
+            bar_sync(1, 256);
+            tc_fence_after();
+            const float2 p0 = c.post[row], p1 = c.post[kTileRows + row];
+            m = fmaxf(p0.x, p1.x);
+            const float mm = m == -INFINITY ? 0.f : m;
+            f0 = ex2((p0.x - mm) * scale);
+            f1 = ex2((p1.x - mm) * scale);
+            l = p0.y * f0 + p1.y * f1;
+            both = count > 1;
+            from = 2 * g;
+            to = from + 2;
+        }
+        const float inv = whole ? 1.f / l : 1.f;
+        f0 *= inv;
+        f1 *= inv;
+        const uint32_t oa = s.two ? oc + g * 128 : oc;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (x < from || x >= to) continue;
+            uint32_t o[32];
+            tmem_ld32(oa + x * 32, o);
+            tmem_wait_ld();
+            tmem_loaded(o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f0);
+            if (both) {
+                uint32_t o1[32];
+                tmem_ld32(oa + 128 + x * 32, o1);
+                tmem_wait_ld();
+                tmem_loaded(o1);
+#pragma unroll
+                for (int y = 0; y < 32; ++y)
+                    o[y] = __float_as_uint(fmaf(__uint_as_float(o1[y]), f1, __uint_as_float(o[y])));
+            }
+            if (valid && whole) {
+                uint4* dst = reinterpret_cast<uint4*>(a.out + ((long)(s.rows + token) * a.Hq + s.kvh * a.G + gi) * kHeadDim) + x * 4;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        v[z] = pack_bf16x2(__uint_as_float(o[y * 8 + z * 2]), __uint_as_float(o[y * 8 + z * 2 + 1]));
+                    dst[y] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            } else if (valid) {
+                uint4* dst = reinterpret_cast<uint4*>(slot_out(a, slot) + (long)(tile * kTileRows + row) * kHeadDim) + x * 8;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[y * 4], o[y * 4 + 1], o[y * 4 + 2], o[y * 4 + 3]);
             }
         }
-        const long row = ((long)page * kPageSize + p % kPageSize) * a.Hkv + kvh;
-        const uint8_t* sc = kFmt == kFmtBf16 ? nullptr : a.scales + scale_offset(page, kvh, p % kPageSize, a.Hkv);
-        float k[4], v[4];
-        load4<kFmt>(a.K, row, sc, l, k);
-        load4<kFmt>(a.V, row, kFmt == kFmtBf16 ? nullptr : sc + kScaleBytes, l, v);
-        float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), c = exp2f(m - mn), w = exp2f(s - mn);
-        m = mn;
-        sum = sum * c + w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * c + w * v[i];
+        if (valid && !whole && (s.two || g == 0)) slot_ml(a, slot)[tile * kTileRows + row] = make_float2(m * scale, l);
+        tc_fence_before();
+        if (!s.two) bar_sync(2, 256);   // both sides have read before either goes on
     }
-    const float r = 1.f / sum;
-    reinterpret_cast<uint2*>(a.out)[(t * a.Hq + h) * 32 + l] =
-        make_uint2(pack_bf16x2(o[0] * r, o[1] * r), pack_bf16x2(o[2] * r, o[3] * r));
+    if (threadIdx.x == 0) {   // does this CTA's last item, begun here, go on in the next one?
+        TailRecord rec = {};
+        if (s.j0 == 0 && s.j1 < s.tiles) {
+            const long long last = u1 - s.j1 + s.tiles - 1;   // the item's last unit
+            rec.valid = 1;
+            rec.rows = s.rows;
+            rec.tokens = s.tokens;
+            rec.kvh = s.kvh;
+            rec.last = (int)(((last + 1) * shares(total) - 1) / total);
+        }
+        reinterpret_cast<TailRecord*>(a.tail)[cta] = rec;
+    }
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
+    chunk_attention_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qm,
+                           const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+    using L = Layout<kFmt>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Control& c = *reinterpret_cast<Control*>(smem + L::kCtl);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&c.q_full[x], 1);
+            mbar_init(&c.q_empty[x], 1);
+            mbar_init(&c.s_full[x], 1);
+            mbar_init(&c.p_full[x], 128);
+            mbar_init(&c.o_full[x], 1);
+        }
+        for (int x = 0; x < L::kStages; ++x) {
+            mbar_init(&c.kv_full[x], L::k8 ? 128 : 1);
+            mbar_init(&c.kv_empty[x], 1);
+        }
+        for (int x = 0; x < L::kRaw; ++x) {
+            mbar_init(&c.raw_full[x], 1);
+            mbar_init(&c.raw_empty[x], 128);
+        }
+        mbar_init(&c.done, 1);
+        c.dead = 0;
+        mbar_fence_init();
+    }
+    if (warp == 9) tmem_alloc(smem_addr(&c.tmem), 512);
+    pdl_enter();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long u0, u1, total;
+    plan(a, c, u0, u1, total);
+    const Walk walk(a, c, u1 - u0);
+    if (warp < 8) {
+        regs_up<L::k8 ? 192 : 216>();
+        softmax_warps(a, c, walk, u1, total);
+    } else if (warp < 12) {
+        regs_down<L::k8 ? 48 : 72>();
+        if (warp == 8) copy_warp<kFmt>(a, c, smem, walk, &qm, &km, &vm);
+        if (warp == 9) mma_warp<kFmt>(a, c, smem, walk);
+    } else if (L::k8) {
+        regs_down<80>();
+        expand_warps<kFmt>(a, c, smem, walk);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(c.tmem, 512);
+}
+
+// Joins the parts of the items that a CTA's border cut: block (c, y) those of the item that began in CTA c,
+// one warp per row, four output dimensions per lane.
+constexpr int kMergeY = 8, kMergeWarpsChunk = 8;
+__global__ void __launch_bounds__(kMergeWarpsChunk * 32) merge_chunks_kernel(const __grid_constant__ ChunkArgs a) {
+    pdl_enter();
+    const TailRecord rec = reinterpret_cast<const TailRecord*>(a.tail)[blockIdx.x];
+    if (!rec.valid) return;
+    const int lane = threadIdx.x & 31, rows = a.tpt * a.G;
+    for (int k = blockIdx.y + kMergeY * (threadIdx.x >> 5); k < rec.tokens * a.G; k += kMergeY * kMergeWarpsChunk) {
+        const int tile = k / rows, r = k - tile * rows, row = tile * kTileRows + r;
+        const int first = 2 * blockIdx.x + 1;   // slots: this CTA's second, then the first of each later CTA
+        float m = slot_ml(a, first)[row].x;
+        for (int x = blockIdx.x + 1; x <= rec.last; ++x) m = fmaxf(m, slot_ml(a, 2 * x)[row].x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 4
+        for (int x = blockIdx.x; x <= rec.last; ++x) {
+            const int slot = x == (int)blockIdx.x ? first : 2 * x;
+            const float2 ml = slot_ml(a, slot)[row];
+            const float4 v = reinterpret_cast<const float4*>(slot_out(a, slot) + (long)row * kHeadDim)[lane];
+            const float f = ex2(ml.x - m);
+            l = fmaf(ml.y, f, l);
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+        }
+        const float inv = 1.f / l;
+        const long dst = ((long)(rec.rows + tile * a.tpt + r / a.G) * a.Hq + rec.kvh * a.G + r % a.G) * 32 + lane;
+        reinterpret_cast<uint2*>(a.out)[dst] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+}
+
+struct Encoder {
+    std::mutex mu;
+    PFN_cuTensorMapEncodeTiled fn = nullptr;
+};
+Encoder g_encoder;
+
+cudaError_t encoder(PFN_cuTensorMapEncodeTiled* out) {
+    std::lock_guard<std::mutex> lock(g_encoder.mu);
+    if (g_encoder.fn == nullptr) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+        g_encoder.fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(fn);
+    }
+    *out = g_encoder.fn;
+    return cudaSuccess;
+}
+
+// [rows][heads][128] with a box of {x values, y heads, z rows}
+bool encode3(PFN_cuTensorMapEncodeTiled fn, CUtensorMap* m, const void* base, bool bytes, long heads, long rows, int x,
+             int y, int z) {
+    const cuuint64_t esz = bytes ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {kHeadDim * esz, kHeadDim * esz * (cuuint64_t)heads};
+    const cuuint32_t box[3] = {(cuuint32_t)x, (cuuint32_t)y, (cuuint32_t)z};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kFmt>
+cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
+    PFN_cuTensorMapEncodeTiled fn;
+    cudaError_t e = encoder(&fn);
+    if (e != cudaSuccess) return e;
+    constexpr bool k8 = Layout<kFmt>::k8;
+    CUtensorMap qm, km, vm;
+    const long rows = (long)a.num_pages * kPageSize;
+    if (!encode3(fn, &qm, a.q, false, a.Hq, a.total_rows, 64, a.G, a.tpt) ||
+        !encode3(fn, &km, a.K, k8, a.Hkv, rows, k8 ? kHeadDim : 64, 1, kPageSize) ||
+        !encode3(fn, &vm, a.V, k8, a.Hkv, rows, k8 ? kHeadDim : 64, 1, kPageSize))
+        return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(chunk_attention_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<kFmt>());
+    if (e != cudaSuccess) return e;
+    const int ctas = a.sms < kChunkCtas ? a.sms : kChunkCtas;
+    e = launch_pdl(chunk_attention_kernel<kFmt>, dim3(ctas), dim3(Layout<kFmt>::kThreads), chunk_smem<kFmt>(), stream, a, qm,
+                   km, vm);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(merge_chunks_kernel, dim3(ctas, kMergeY), dim3(kMergeWarpsChunk * 32), 0, stream, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+ChunkLayout chunk_layout() {
+    ChunkLayout L;
+    L.part = 0;
+    L.ml = (size_t)2 * kChunkCtas * 2 * kTileRows * kHeadDim * sizeof(float);
+    L.tail = L.ml + (size_t)2 * kChunkCtas * 2 * kTileRows * sizeof(float2);
+    L.total = (L.tail + kChunkCtas * sizeof(TailRecord) + 255) / 256 * 256;
+    return L;
 }
 
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream) {
-    const dim3 grid((unsigned)(((long)a.total_rows * a.Hq + 3) / 4)), block(128);
-    const size_t smem = sizeof(int) * (a.B + 1);
-    cudaError_t e = format == kFmtBf16 ? launch_pdl(chunk_attention_kernel<kFmtBf16>, grid, block, smem, stream, a)
-                    : format == kFmtFp8 ? launch_pdl(chunk_attention_kernel<kFmtFp8>, grid, block, smem, stream, a)
-                                        : launch_pdl(chunk_attention_kernel<kFmtInt8>, grid, block, smem, stream, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return format == kFmtBf16 ? launch_format<kFmtBf16>(a, stream)
+           : format == kFmtFp8 ? launch_format<kFmtFp8>(a, stream) : launch_format<kFmtInt8>(a, stream);
 }
 
 }  // namespace sd

@@ -184,10 +184,20 @@ struct ChunkArgs {
     const int32_t* row_start;
     __nv_bfloat16* out;       // [total_rows][Hq][128]
     int32_t* status;
+    // workspace: the parts of items that a CTA's border cuts, two slots of 256 rows per CTA
+    float* part;              // un-normalised outputs
+    float2* ml;               // maximum (log2 units) and sum of each row
+    void* tail;               // per CTA: the item that goes on in later CTAs
     int B, Hq, Hkv, G, max_pages, num_pages, total_rows, sms;
+    int tpt;                  // tokens to a tile of 128 rows: 128 / G
     long n_cap;
     float scale_log2;         // log2(e) / sqrt(d)
 };
+constexpr int kChunkCtas = 160;   // persistent CTAs at most
+struct ChunkLayout {
+    size_t part, ml, tail, total;
+};
+ChunkLayout chunk_layout();
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream);
 
 // Sparse decode over an 8-bit cache (cache_sparse.cu).

@@ -60,12 +60,29 @@ struct Layout {
     static constexpr int kThreads = k8 ? 512 : 384;
 };
 
+constexpr int kSegments = 4;   // stretches that the copies may run ahead
+
+// One stretch of consecutive units of one item.
+struct Segment {
+    int b, kvh;
+    int rows;     // first row (token) of the item in q and out
+    int tokens;   // tokens of the item
+    int first;    // position of its first token
+    int end;      // positions that its last token sees
+    int j0, j1;   // key/value tiles of the stretch (none: the share has ended)
+    int tiles;    // key/value tiles of the item
+    int last;     // the CTA that has the item's last unit, if the item begins here and goes on there, else -1
+    int two;      // the item has a second tile of rows
+};
+
 struct Control {
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[5], kv_empty[5];
     uint64_t raw_full[3], raw_empty[3];
     uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t done;
+    uint64_t join[2], done;
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
+    Segment seg[kSegments];
     uint32_t tmem;
     int dead;                // a wait ran out: nothing more is issued
     int b, kvh, pair, unit;  // where this CTA's share starts
@@ -127,25 +144,17 @@ __device__ __forceinline__ long long tiles_before(const Request& r, int i, int i
     return sum;
 }
 
-// One stretch of consecutive units of one item.
-struct Segment {
-    int b, kvh;
-    int rows;     // first row (token) of the item in q and out
-    int tokens;   // tokens of the item
-    int first;    // position of its first token
-    int end;      // positions that its last token sees
-    int j0, j1;   // key/value tiles of the stretch
-    int tiles;    // key/value tiles of the item
-    bool two;     // the item has a second tile of rows
-};
+// CTAs that get units: each of them at least one, so that the parts of a cut item lie in neighbouring CTAs.
+__device__ __forceinline__ long long shares(long long total) { return min(total, (long long)gridDim.x); }
 
+// A CTA's share as stretches, for the copy warp.
 struct Walk {
     const ChunkArgs& a;
     int w, b, kvh, i, j, items;
-    long long left;
+    long long left, u1, total;
     Request r;
-    __device__ Walk(const ChunkArgs& args, const Control& c, long long units)
-        : a(args), w(2 * args.tpt), b(c.b), kvh(c.kvh), i(c.pair), j(c.unit), left(units) {
+    __device__ Walk(const ChunkArgs& args, const Control& c, long long begin, long long end, long long all)
+        : a(args), w(2 * args.tpt), b(c.b), kvh(c.kvh), i(c.pair), j(c.unit), left(end - begin), u1(end), total(all) {
         if (left > 0) {
             r = request(a, b);
             items = (r.n + w - 1) / w;
@@ -162,8 +171,11 @@ struct Walk {
         s.tiles = (s.end + kTileRows - 1) / kTileRows;
         s.j0 = j;
         s.j1 = (int)min((long long)s.tiles, j + left);
-        s.two = s.tokens > a.tpt;
+        s.two = s.tokens > a.tpt ? 1 : 0;
         left -= s.j1 - s.j0;
+        s.last = -1;
+        if (left == 0 && s.j0 == 0 && s.j1 < s.tiles)
+            s.last = (int)(((u1 - s.j1 + s.tiles) * shares(total) - 1) / total);
         j = s.j1;
         if (left > 0) {   // the stretch ended with its item
             j = 0;
@@ -191,9 +203,6 @@ __device__ __forceinline__ float* slot_out(const ChunkArgs& a, int slot) {
     return a.part + (long)slot * (2 * kTileRows) * kHeadDim;
 }
 __device__ __forceinline__ float2* slot_ml(const ChunkArgs& a, int slot) { return a.ml + (long)slot * (2 * kTileRows); }
-
-// CTAs that get units: each of them at least one, so that the parts of a cut item lie in neighbouring CTAs.
-__device__ __forceinline__ long long shares(long long total) { return min(total, (long long)gridDim.x); }
 
 // The block's share [u0, u1) of the batch's units, its start in `c`, and the checks of row_start and lens.
 // False where row_start is not valid (nothing is done then).
@@ -267,6 +276,26 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
     return true;
 }
 
+// The stretches in order, as the copy warp hands them out; one arrival per warp gives a slot back.
+struct Stretches {
+    Control& c;
+    int32_t* status;
+    uint32_t n;
+    __device__ Stretches(Control& control, int32_t* st) : c(control), status(st), n(0) {}
+    __device__ __forceinline__ const Segment* next() {   // null: no more
+        const uint32_t slot = n % kSegments;
+        bool ok = pipe_wait(&c.seg_full[slot], (n / kSegments) & 1, &c.dead, status);
+        ok = __all_sync(0xffffffffu, ok);
+        const Segment* s = &c.seg[slot];
+        return ok && s->j1 > s->j0 ? s : nullptr;
+    }
+    __device__ __forceinline__ void done() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&c.seg_empty[n % kSegments]);
+        ++n;
+    }
+};
+
 // ---- warp 8: copies -------------------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -286,9 +315,20 @@ __device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_
     uint64_t* empty = L::k8 ? c.raw_empty : c.kv_empty;
     const uint32_t base = smem_addr(smem);
     const int my = L::k8 ? (lane & 7) : (lane >> 1) & 7;   // the page of the tile that this lane copies
-    uint32_t ring = 0, q_count[2] = {0, 0}, unit_count = 0;
+    uint32_t ring = 0, q_count[2] = {0, 0}, unit_count = 0, segments = 0;
     Segment s;
-    while (walk.next(s)) {
+    for (bool more = true; more;) {
+        more = walk.next(s);
+        if (!more) s.j0 = s.j1 = 0;
+        const uint32_t slot = segments % kSegments;
+        pipe_wait(&c.seg_empty[slot], ((segments / kSegments) & 1) ^ 1, &c.dead, a.status);
+        ++segments;
+        if (lane == 0) {
+            c.seg[slot] = s;
+            mbar_arrive(&c.seg_full[slot]);
+        }
+        __syncwarp();
+        if (!more) break;
         for (int t = 0; t < (s.two ? 2 : 1); ++t) {
             const bool ok = pipe_wait(&c.q_empty[t], (q_count[t] & 1) ^ 1, &c.dead, a.status);
             ++q_count[t];
@@ -369,13 +409,13 @@ __device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_
 
 // ---- warp 9: MMAs -----------------------------------------------------------------------------------------
 template <int kFmt>
-__device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t* smem, Walk walk) {
+__device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t* smem) {
     using L = Layout<kFmt>;
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem), tm = c.tmem;
     constexpr uint32_t kQk = mma_idesc(128, 128, false), kPv = mma_idesc(128, 128, true);
     uint32_t ring = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
-    Segment s;
+    Stretches stretches(c, a.status);
 
     auto wait_stage = [&]() -> uint32_t {   // the next stage of the ring, full
         const uint32_t st = ring % L::kStages;
@@ -413,8 +453,7 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
         __syncwarp();
     };
     // The value rows behind the item's last position are zeroed: their weights are zero, and 0 * NaN is NaN.
-    auto clear_tail = [&](uint32_t st, int t) {
-        const int from = s.end - (s.j0 + t) * kTileRows;
+    auto clear_tail = [&](uint32_t st, int from) {
         if (L::k8 || from >= kTileRows) return;
         uint8_t* v = smem + L::kKv + st * kStageBytes;
         for (int x = from * 8 + lane; x < kTileRows * 8; x += 32) {
@@ -425,11 +464,11 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
         __syncwarp();
     };
 
-    while (walk.next(s)) {
-        const int count = s.j1 - s.j0;
+    while (const Segment* s = stretches.next()) {
+        const int count = s->j1 - s->j0, end = s->end - s->j0 * kTileRows, two = s->two;
         pipe_wait(&c.q_full[0], q_count[0] & 1, &c.dead, a.status);
         ++q_count[0];
-        if (s.two) {
+        if (two) {
             pipe_wait(&c.q_full[1], q_count[1] & 1, &c.dead, a.status);
             ++q_count[1];
             uint32_t k = wait_stage();
@@ -439,7 +478,7 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
             for (int t = 0; t < count; ++t) {
                 const uint32_t v = wait_stage();
                 const bool more = t + 1 < count;
-                clear_tail(v, t);
+                clear_tail(v, end - t * kTileRows);
                 if (more) k = wait_stage();
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -461,7 +500,7 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
             for (int t = 0; t < count; ++t) {
                 const int g = t & 1;
                 const uint32_t v = wait_stage();
-                clear_tail(v, t);
+                clear_tail(v, end - t * kTileRows);
                 pv(g, v, t > 1);
                 commit(&c.kv_empty[v]);
                 if (t + 2 < count) {
@@ -474,6 +513,7 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
             }
             commit(&c.q_empty[0]);
         }
+        stretches.done();
     }
     if (lane == 0) mma_commit(&c.done);   // everything issued has ended before tensor memory is given back
     __syncwarp();
@@ -482,12 +522,12 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
 
 // ---- warps 12-15 (8-bit caches): raw tiles to bf16 stages -------------------------------------------------
 template <int kFmt>
-__device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uint8_t* smem, Walk walk) {
+__device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uint8_t* smem) {
     using L = Layout<kFmt>;
     const int tid = threadIdx.x & 127;
     uint32_t ring = 0, unit[2] = {0, 0};
-    Segment s;
-    auto tile = [&](bool v, int t) {
+    Stretches stretches(c, a.status);
+    auto tile = [&](bool v, int rows) {   // rows from there on become zero
         const uint32_t raw = ring % L::kRaw, st = ring % L::kStages;
         pipe_wait(&c.raw_full[raw], (ring / L::kRaw) & 1, &c.dead, a.status);
         pipe_wait(&c.kv_empty[st], ((ring / L::kStages) & 1) ^ 1, &c.dead, a.status);
@@ -497,7 +537,6 @@ __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uin
         ++unit[v];
         uint8_t* dst = smem + L::kKv + st * kStageBytes;
         const int c16 = tid & 7, h = c16 >> 2;
-        const int rows = min(kTileRows, s.end - (s.j0 + t) * kTileRows);   // rows behind them become zero
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
             const int row = x * 16 + (tid >> 3);
@@ -520,28 +559,31 @@ __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uin
         mbar_arrive(&c.kv_full[st]);
         mbar_arrive(&c.raw_empty[raw]);
     };
-    while (walk.next(s)) {
-        const int count = s.j1 - s.j0, ahead = s.two ? 1 : 2;
-        tile(false, 0);
-        if (ahead == 2 && count > 1) tile(false, 1);
+    while (const Segment* s = stretches.next()) {
+        const int count = s->j1 - s->j0, ahead = s->two ? 1 : 2, end = s->end - s->j0 * kTileRows;
+        tile(false, end);
+        if (ahead == 2 && count > 1) tile(false, end - kTileRows);
         for (int t = 0; t < count; ++t) {
-            tile(true, t);
-            if (t + ahead < count) tile(false, t + ahead);
+            tile(true, end - t * kTileRows);
+            if (t + ahead < count) tile(false, end - (t + ahead) * kTileRows);
         }
+        stretches.done();
     }
 }
 
 // ---- warps 0-7: softmax and output --------------------------------------------------------------------------
-__device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c, Walk walk, long long u1, long long total) {
+__device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
     const int cta = blockIdx.x;
     const int g = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const uint32_t sc = c.tmem + g * 128 + lanes, oc = c.tmem + 256 + lanes;
     const int tq = row / a.G, gi = row - tq * a.G;
     const float scale = a.scale_log2;
-    uint32_t s_count = 0, o_count = 0;
-    Segment s = {};
-    while (walk.next(s)) {
+    uint32_t s_count = 0, o_count = 0, joins = 0;
+    Stretches stretches(c, a.status);
+    if (threadIdx.x == 0) reinterpret_cast<TailRecord*>(a.tail)[cta] = TailRecord{};
+    while (const Segment* seg = stretches.next()) {
+        const Segment& s = *seg;
         const int tile = s.two ? g : 0, step = s.two ? 1 : 2, count = s.j1 - s.j0;
         const int token = tile * a.tpt + tq;
         const bool valid = tq < a.tpt && token < s.tokens;
@@ -643,7 +685,9 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c, Wa
         if (!s.two) {
             c.post[g * kTileRows + row] = make_float2(m, l);
             tc_fence_before();
-            bar_sync(1, 256);
+            mbar_arrive(&c.join[0]);
+            pipe_wait(&c.join[0], joins & 1, &c.dead, a.status);
+            __syncwarp();
             tc_fence_after();
             const float2 p0 = c.post[row], p1 = c.post[kTileRows + row];
             m = fmaxf(p0.x, p1.x);
@@ -695,19 +739,15 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c, Wa
         }
         if (valid && !whole && (s.two || g == 0)) slot_ml(a, slot)[tile * kTileRows + row] = make_float2(m * scale, l);
         tc_fence_before();
-        if (!s.two) bar_sync(2, 256);   // both sides have read before either goes on
-    }
-    if (threadIdx.x == 0) {   // does this CTA's last item, begun here, go on in the next one?
-        TailRecord rec = {};
-        if (s.j0 == 0 && s.j1 < s.tiles) {
-            const long long last = u1 - s.j1 + s.tiles - 1;   // the item's last unit
-            rec.valid = 1;
-            rec.rows = s.rows;
-            rec.tokens = s.tokens;
-            rec.kvh = s.kvh;
-            rec.last = (int)(((last + 1) * shares(total) - 1) / total);
+        if (!s.two) {   // both sides have read before either goes on
+            mbar_arrive(&c.join[1]);
+            pipe_wait(&c.join[1], joins & 1, &c.dead, a.status);
+            ++joins;
+            __syncwarp();
         }
-        reinterpret_cast<TailRecord*>(a.tail)[cta] = rec;
+        if (threadIdx.x == 0 && s.last >= 0)
+            reinterpret_cast<TailRecord*>(a.tail)[cta] = TailRecord{1, s.rows, s.tokens, s.kvh, s.last, {}};
+        stretches.done();
     }
 }
 
@@ -726,6 +766,7 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
             mbar_init(&c.s_full[x], 1);
             mbar_init(&c.p_full[x], 128);
             mbar_init(&c.o_full[x], 1);
+            mbar_init(&c.join[x], 256);
         }
         for (int x = 0; x < L::kStages; ++x) {
             mbar_init(&c.kv_full[x], L::k8 ? 128 : 1);
@@ -734,6 +775,10 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
         for (int x = 0; x < L::kRaw; ++x) {
             mbar_init(&c.raw_full[x], 1);
             mbar_init(&c.raw_empty[x], 128);
+        }
+        for (int x = 0; x < kSegments; ++x) {
+            mbar_init(&c.seg_full[x], 1);
+            mbar_init(&c.seg_empty[x], L::k8 ? 13 : 9);   // the warps that read them
         }
         mbar_init(&c.done, 1);
         c.dead = 0;
@@ -746,17 +791,16 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     tc_fence_after();
     long long u0, u1, total;
     plan(a, c, u0, u1, total);
-    const Walk walk(a, c, u1 - u0);
     if (warp < 8) {
         regs_up<L::k8 ? 192 : 216>();
-        softmax_warps(a, c, walk, u1, total);
+        softmax_warps(a, c);
     } else if (warp < 12) {
         regs_down<L::k8 ? 48 : 72>();
-        if (warp == 8) copy_warp<kFmt>(a, c, smem, walk, &qm, &km, &vm);
-        if (warp == 9) mma_warp<kFmt>(a, c, smem, walk);
+        if (warp == 8) copy_warp<kFmt>(a, c, smem, Walk(a, c, u0, u1, total), &qm, &km, &vm);
+        if (warp == 9) mma_warp<kFmt>(a, c, smem);
     } else if (L::k8) {
         regs_down<80>();
-        expand_warps<kFmt>(a, c, smem, walk);
+        expand_warps<kFmt>(a, c, smem);
     }
     tc_fence_before();
     __syncthreads();

@@ -104,11 +104,6 @@ template <int N>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
-// Named barrier over `threads` threads of the block.
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
-}
-
 // ---- fp32 pairs and the base-2 exponential --------------------------------------------------------------
 __device__ __forceinline__ float ex2(float x) {
     float r;

@@ -88,6 +88,16 @@ __device__ __forceinline__ Factor factor_of(uint32_t byte) {
     return f;
 }
 
+// Bytes whose factor is one normal bf16 (nearly all: e from -124 to 7, or from -126 to 121), and that factor.
+template <int kFmt>
+__device__ __forceinline__ bool plain_factor(uint32_t byte) {
+    return kFmt == kFmtFp8 ? byte <= 134u : byte - 7u <= 247u;
+}
+template <int kFmt>
+__device__ __forceinline__ uint32_t factor_plain(uint32_t byte) {
+    return (kFmt == kFmtFp8 ? byte + 120u : byte - 6u) * 0x00800080u;
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -44,6 +44,10 @@ constexpr int kHalf = 16 * 1024;               // 128 rows of 64 bf16 values
 constexpr int kStageBytes = 2 * kHalf;         // a K or V tile in bf16
 constexpr int kRawBytes = 16 * 1024;           // the same in 8 bits
 constexpr int kScaleTile = 1024;               // scales of K and V of 128 positions
+#ifndef FMAOF8
+#define FMAOF8 0
+#endif
+constexpr int kFmaOf8 = FMAOF8;                      // of eight pairs of weights, those computed on the FMA pipe
 constexpr float kRescale = 8.f;                // log2 units that the maximum may lag behind
 
 template <int kFmt>
@@ -96,14 +100,19 @@ constexpr int chunk_smem() {
 }
 static_assert(chunk_smem<kFmtBf16>() <= 227 * 1024 && chunk_smem<kFmtFp8>() <= 227 * 1024, "shared memory");
 
-// A bounded wait; once one has run out, every later one returns at once.
+// A bounded wait; once one has run out, every later one gives up soon.  (The timer and the flag are looked at now
+// and then: reading them in every round costs latency.)
 __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* status) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     for (uint32_t it = 0; it < kWaitLimitIters; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*reinterpret_cast<volatile int*>(dead)) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) break;
+        if ((it & 31) == 31) {
+            if (*reinterpret_cast<volatile int*>(dead)) return false;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) break;
+        }
     }
     *reinterpret_cast<volatile int*>(dead) = 1;
     report(status, SD_ERR_TIMEOUT);
@@ -412,7 +421,7 @@ template <int kFmt>
 __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t* smem) {
     using L = Layout<kFmt>;
     const int lane = threadIdx.x & 31;
-    const uint32_t base = smem_addr(smem), tm = c.tmem;
+    const uint32_t base = smem_addr(smem), tm = uniform(c.tmem);
     constexpr uint32_t kQk = mma_idesc(128, 128, false), kPv = mma_idesc(128, 128, true);
     uint32_t ring = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
     Stretches stretches(c, a.status);
@@ -421,36 +430,28 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
         const uint32_t st = ring % L::kStages;
         pipe_wait(&c.kv_full[st], (ring / L::kStages) & 1, &c.dead, a.status);
         ++ring;
+        __syncwarp();
         return st;
     };
-    auto live = [&]() { return *reinterpret_cast<volatile int*>(&c.dead) == 0; };
     auto qk = [&](int g, int tile, uint32_t st) {
-        const uint32_t q = base + L::kQ + tile * kStageBytes, k = base + L::kKv + st * kStageBytes;
-        if (lane == 0 && live()) {
+        const uint32_t qd = smem_desc(base + L::kQ + tile * kStageBytes, 16);
+        const uint32_t kd = smem_desc(base + L::kKv + st * kStageBytes, 16);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint32_t off = (x >> 2) * kHalf + (x & 3) * 32;
-                mma_ss(tm + g * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kQk, x > 0);
-            }
-            mma_commit(&c.s_full[g]);
+        for (int x = 0; x < 8; ++x) {   // (a descriptor counts its address in 16 bytes)
+            const uint32_t off = ((x >> 2) * kHalf + (x & 3) * 32) >> 4;
+            mma_ss(tm + g * 128, qd + off, kd + off, kQk, x > 0);
         }
-        __syncwarp();
+        mma_commit(&c.s_full[g]);
     };
     auto pv = [&](int g, uint32_t st, bool add) {
-        const uint32_t v = base + L::kKv + st * kStageBytes;
+        const uint32_t vd = smem_desc(base + L::kKv + st * kStageBytes, kHalf);
         pipe_wait(&c.p_full[g], p_count[g] & 1, &c.dead, a.status);
         ++p_count[g];
+        __syncwarp();
         tc_fence_after();
-        if (lane == 0 && live()) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                mma_ts(tm + 256 + g * 128, tm + g * 128 + x * 8, smem_desc(v + x * 2048, kHalf, 1024), kPv, add || x > 0);
-        }
-        __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-        if (lane == 0 && live()) mma_commit(bar);
-        __syncwarp();
+        for (int x = 0; x < 8; ++x)
+            mma_ts(tm + 256 + g * 128, tm + g * 128 + x * 8, vd + x * (2048 >> 4), kPv, add || x > 0);
     };
     // The value rows behind the item's last position are zeroed: their weights are zero, and 0 * NaN is NaN.
     auto clear_tail = [&](uint32_t st, int from) {
@@ -465,7 +466,7 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
     };
 
     while (const Segment* s = stretches.next()) {
-        const int count = s->j1 - s->j0, end = s->end - s->j0 * kTileRows, two = s->two;
+        const int count = uniform(s->j1 - s->j0), end = uniform(s->end - s->j0 * kTileRows), two = uniform(s->two);
         pipe_wait(&c.q_full[0], q_count[0] & 1, &c.dead, a.status);
         ++q_count[0];
         if (two) {
@@ -474,7 +475,7 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
             uint32_t k = wait_stage();
             qk(0, 0, k);
             qk(1, 1, k);
-            commit(&c.kv_empty[k]);
+            mma_commit(&c.kv_empty[k]);
             for (int t = 0; t < count; ++t) {
                 const uint32_t v = wait_stage();
                 const bool more = t + 1 < count;
@@ -483,39 +484,39 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     pv(g, v, t > 0);
-                    if (g == 1) commit(&c.kv_empty[v]);
+                    if (g == 1) mma_commit(&c.kv_empty[v]);
                     if (more) qk(g, g, k);
-                    else commit(&c.o_full[g]);
+                    else mma_commit(&c.o_full[g]);
                 }
-                if (more) commit(&c.kv_empty[k]);
+                if (more) mma_commit(&c.kv_empty[k]);
             }
-            commit(&c.q_empty[0]);
-            commit(&c.q_empty[1]);
+            mma_commit(&c.q_empty[0]);
+            mma_commit(&c.q_empty[1]);
         } else {
             for (int g = 0; g < 2 && g < count; ++g) {
                 const uint32_t k = wait_stage();
                 qk(g, 0, k);
-                commit(&c.kv_empty[k]);
+                mma_commit(&c.kv_empty[k]);
             }
             for (int t = 0; t < count; ++t) {
                 const int g = t & 1;
                 const uint32_t v = wait_stage();
                 clear_tail(v, end - t * kTileRows);
                 pv(g, v, t > 1);
-                commit(&c.kv_empty[v]);
+                mma_commit(&c.kv_empty[v]);
                 if (t + 2 < count) {
                     const uint32_t k = wait_stage();
                     qk(g, 0, k);
-                    commit(&c.kv_empty[k]);
+                    mma_commit(&c.kv_empty[k]);
                 } else {
-                    commit(&c.o_full[g]);
+                    mma_commit(&c.o_full[g]);
                 }
             }
-            commit(&c.q_empty[0]);
+            mma_commit(&c.q_empty[0]);
         }
         stretches.done();
     }
-    if (lane == 0) mma_commit(&c.done);   // everything issued has ended before tensor memory is given back
+    mma_commit(&c.done);   // everything issued has ended before tensor memory is given back
     __syncwarp();
     mbar_wait(&c.done, 0);
 }
@@ -536,24 +537,49 @@ __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uin
         const uint8_t* sc = smem + L::kScaleOff + (unit[v] % 3) * kScaleTile + (v ? kScaleBytes : 0);
         ++unit[v];
         uint8_t* dst = smem + L::kKv + st * kStageBytes;
-        const int c16 = tid & 7, h = c16 >> 2;
+        const int c16 = tid & 7, h = c16 >> 2, k0 = 2 * (c16 & 3);
+        // lanes of the upper half write their second chunk first: eight lanes, eight bank groups
+        auto put = [&](int row, const uint4& o0, const uint4& o1) {
+            uint8_t* line = dst + h * kHalf + row * 128;
+            *reinterpret_cast<uint4*>(line + (((k0 + h) ^ (row & 7)) << 4)) = h ? o1 : o0;
+            *reinterpret_cast<uint4*>(line + (((k0 + 1 - h) ^ (row & 7)) << 4)) = h ? o0 : o1;
+        };
+        uint32_t by[8];
+        bool plain = rows >= kTileRows;
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const int row = x * 16 + (tid >> 3);
-            uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-            if (row < rows) {
+            by[x] = sc[(x * 16 + (tid >> 3)) * (2 * kScaleBytes) + (c16 >> 1)];
+            plain = plain && plain_factor<kFmt>(by[x]);
+        }
+        if (__all_sync(0xffffffffu, plain)) {   // straight-line: the loads and the arithmetic of all rows overlap
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int row = x * 16 + (tid >> 3);
                 const uint4 e = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
-                const Factor f = factor_of<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
-                decode4<kFmt>(e.x, f, o[0].x, o[0].y);
-                decode4<kFmt>(e.y, f, o[0].z, o[0].w);
-                decode4<kFmt>(e.z, f, o[1].x, o[1].y);
-                decode4<kFmt>(e.w, f, o[1].z, o[1].w);
+                const uint32_t f = factor_plain<kFmt>(by[x]);
+                uint4 o0, o1;
+                expand4<kFmt>(e.x, o0.x, o0.y);
+                expand4<kFmt>(e.y, o0.z, o0.w);
+                expand4<kFmt>(e.z, o1.x, o1.y);
+                expand4<kFmt>(e.w, o1.z, o1.w);
+                put(row, make_uint4(mul_bf16x2(o0.x, f), mul_bf16x2(o0.y, f), mul_bf16x2(o0.z, f), mul_bf16x2(o0.w, f)),
+                    make_uint4(mul_bf16x2(o1.x, f), mul_bf16x2(o1.y, f), mul_bf16x2(o1.z, f), mul_bf16x2(o1.w, f)));
             }
-            // lanes of the upper half write their second chunk first: eight lanes, eight bank groups
-            uint8_t* line = dst + h * kHalf + row * 128;
-            const int k0 = 2 * (c16 & 3);
-            *reinterpret_cast<uint4*>(line + (((k0 + h) ^ (row & 7)) << 4)) = h ? o[1] : o[0];
-            *reinterpret_cast<uint4*>(line + (((k0 + 1 - h) ^ (row & 7)) << 4)) = h ? o[0] : o[1];
+        } else {   // the item's last tile, or a scale at the ends of the range
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) {
+                const int row = x * 16 + (tid >> 3);
+                uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;
+                if (row < rows) {
+                    const uint4 e = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
+                    const Factor f = factor_of<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
+                    decode4<kFmt>(e.x, f, o0.x, o0.y);
+                    decode4<kFmt>(e.y, f, o0.z, o0.w);
+                    decode4<kFmt>(e.z, f, o1.x, o1.y);
+                    decode4<kFmt>(e.w, f, o1.z, o1.w);
+                }
+                put(row, o0, o1);
+            }
         }
         fence_proxy_async();
         mbar_arrive(&c.kv_full[st]);
@@ -589,34 +615,46 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
         const bool valid = tq < a.tpt && token < s.tokens;
         const int lim = valid ? s.first + token : s.end - 1;   // last position that the row sees
         const int lowest = s.first + tile * a.tpt;             // least of these in the tile
+        const bool rows_here = __any_sync(0xffffffffu, valid);   // else the warp only keeps the barriers going
         float m = -INFINITY, l = 0.f;
         bool begun = false;
         for (int t = s.two ? 0 : g; t < count; t += step) {
             bool ok = pipe_wait(&c.s_full[g], s_count & 1, &c.dead, a.status);
             ++s_count;
             if (!__all_sync(0xffffffffu, ok)) continue;
+            if (!rows_here) {
+                mbar_arrive(&c.p_full[g]);
+                continue;
+            }
             tc_fence_after();
             uint32_t r[4][32];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(sc + x * 32, r[x]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_loaded(r[x]);
-            const int col0 = (s.j0 + t) * kTileRows;
-            if (col0 + kTileRows - 1 > lowest) {
-                const int last = lim - col0;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int y = 0; y < 32; ++y)
-                        if (x * 32 + y > last) r[x][y] = 0xff800000u;
-            }
+            tmem_ld32(sc, r[0]);
+            tmem_ld32(sc + 32, r[1]);
+            const int col0 = (s.j0 + t) * kTileRows, last = lim - col0;
+            const bool border = col0 + kTileRows - 1 > lowest;
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int h = 0; h < 2; ++h) {   // the second half arrives while the first one is looked at
+                tmem_wait_ld();
+                tmem_loaded(r[2 * h]);
+                tmem_loaded(r[2 * h + 1]);
+                if (h == 0) {
+                    tmem_ld32(sc + 64, r[2]);
+                    tmem_ld32(sc + 96, r[3]);
+                }
 #pragma unroll
-                for (int y = 0; y < 32; y += 2)
-                    mx[x] = max3(mx[x], __uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1]));
+                for (int x = 2 * h; x < 2 * h + 2; ++x) {
+                    if (border) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (x * 32 + y > last) r[x][y] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2)
+                        mx[2 * (x & 1) + ((y >> 1) & 1)] =
+                            max3(mx[2 * (x & 1) + ((y >> 1) & 1)], __uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1]));
+                }
+            }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             const bool grow = (top - m) * scale > kRescale;   // (from -infinity: any finite score)
             if (__any_sync(0xffffffffu, grow)) {
@@ -648,16 +686,23 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                uint32_t p[32];
+                uint32_t(&p)[32] = r[x * 2];   // pair y takes the place of values that were used before
 #pragma unroll
                 for (int y = 0; y < 32; ++y) {
                     const uint32_t(&src)[32] = r[x * 2 + (y >> 4)];
                     const int z = (y & 15) * 2;
+                    uint64_t e = fma2(pair_of(__uint_as_float(src[z]), __uint_as_float(src[z + 1])), sc2, sh2);
                     float lo, hi;
-                    split_pair(fma2(pair_of(__uint_as_float(src[z]), __uint_as_float(src[z + 1])), sc2, sh2), lo, hi);
-                    lo = ex2(lo);
-                    hi = ex2(hi);
-                    sum[y & 1] = add2(sum[y & 1], pair_of(lo, hi));
+                    if ((y & 7) < kFmaOf8) {
+                        e = ex2_fma2(e);
+                        split_pair(e, lo, hi);
+                    } else {
+                        split_pair(e, lo, hi);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        e = pair_of(lo, hi);
+                    }
+                    sum[y & 1] = add2(sum[y & 1], e);
                     p[y] = pack_bf16x2(lo, hi);
                 }
                 tmem_st32(sc + x * 32, p);
@@ -705,7 +750,7 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
         const uint32_t oa = s.two ? oc + g * 128 : oc;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            if (x < from || x >= to) continue;
+            if (!rows_here || x < from || x >= to) continue;
             uint32_t o[32];
             tmem_ld32(oa + x * 32, o);
             tmem_wait_ld();
@@ -792,14 +837,14 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     long long u0, u1, total;
     plan(a, c, u0, u1, total);
     if (warp < 8) {
-        regs_up<L::k8 ? 192 : 216>();
+        regs_up<L::k8 ? 200 : 216>();
         softmax_warps(a, c);
     } else if (warp < 12) {
         regs_down<L::k8 ? 48 : 72>();
         if (warp == 8) copy_warp<kFmt>(a, c, smem, Walk(a, c, u0, u1, total), &qm, &km, &vm);
         if (warp == 9) mma_warp<kFmt>(a, c, smem);
     } else if (L::k8) {
-        regs_down<80>();
+        regs_down<64>();
         expand_warps<kFmt>(a, c, smem);
     }
     tc_fence_before();

@@ -61,36 +61,45 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 //   K-major (values run along the contraction): `lead` is not used, `stride` = bytes between 8-row groups.
 //   MN-major (values run along the result's dimension, rows along the contraction): `lead` = bytes between
 //   64-value blocks of the result's dimension, `stride` = bytes between groups of 8 contraction steps.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// The lower word holds the address (in 16 bytes: a tile's other parts are reached by adding to it) and `lead`, the
+// upper word is the same for all tiles here.
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t lead) {
+    return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kDescUpper = (1024u >> 4) | (1u << 14) | (2u << 29);
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N, A K-major, B K-major or (b_mn) MN-major.
 constexpr uint32_t mma_idesc(int m, int n, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
 
-// D (tensor memory) = A B (+ D), 16 steps of the contraction; issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// D (tensor memory) = A B (+ D), 16 steps of the contraction.  The whole warp calls, converged and with the same
+// arguments, and one elected lane issues: so the operands stay in uniform registers (issued inside a branch for one
+// lane, each operand is moved there for each MMA, which took twice the MMAs' own time).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n mov.b64 da, {%1, %5};\n"
+        " mov.b64 db, {%2, %5};\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(kDescUpper)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        "{\n .reg .pred p, e;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+        " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(kDescUpper)
         : "memory");
 }
-// One arrival on `bar` when every MMA that this thread issued so far is done.
+// One arrival on `bar` when every MMA that the elected lane issued so far is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
+        : "memory");
 }
+// A value that is the same in all lanes, marked as such.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Writes to shared memory by ordinary stores become visible to the tensor cores and to bulk copies.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
@@ -132,6 +141,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// 2^x of two values on the FMA pipe, for x <= 126: x = n + f with f in [-1/2, 1/2], 2^f by the polynomial of degree 4 whose
+// largest relative error is least (2.7e-6, from the exchange algorithm on 2^f), n added to the exponent.
+// Adding 1.5 * 2^23 rounds to the integer n and leaves it in the low bits.  Below -126 the result is about 2^-126.
+__device__ __forceinline__ uint64_t ex2_fma2(uint64_t x) {
+    float lo, hi;
+    split_pair(x, lo, hi);
+    x = pair_of(fmaxf(lo, -126.f), fmaxf(hi, -126.f));
+    const uint64_t magic = pair_of(12582912.f, 12582912.f), back = pair_of(-12582912.f, -12582912.f);
+    const uint64_t t = add2(x, magic);
+    const uint64_t f = fma2(add2(t, back), pair_of(-1.f, -1.f), x);
+    uint64_t p = pair_of(0.009570102207362652f, 0.009570102207362652f);
+    p = fma2(p, f, pair_of(0.05591785907745361f, 0.05591785907745361f));
+    p = fma2(p, f, pair_of(0.240247443318367f, 0.240247443318367f));
+    p = fma2(p, f, pair_of(0.6931217908859253f, 0.6931217908859253f));
+    p = fma2(p, f, pair_of(0.9999992847442627f, 0.9999992847442627f));
+    float tl, th, pl, ph;
+    split_pair(t, tl, th);
+    split_pair(p, pl, ph);
+    return pair_of(__uint_as_float(__float_as_uint(pl) + (__float_as_uint(tl) << 23)),
+                   __uint_as_float(__float_as_uint(ph) + (__float_as_uint(th) << 23)));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;

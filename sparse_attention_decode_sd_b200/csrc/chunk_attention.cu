@@ -14,7 +14,7 @@
 // One CTA, warp-specialised around tensor memory (512 columns: scores of the two tiles, outputs of the two
 // tiles), with
 //   warps 0-3, 4-7   softmax of tile 0 and tile 1, one row per thread
-//   warp 8           copies: K and V page by page (one TMA box of 16 rows x 64 values per page and half, in
+//   warps 8, 10      copies: K and V page by page (one TMA box of 16 rows x 64 values per page and half, in
 //                    the 128-byte swizzle, into a ring of 32 KB stages), the two tiles of q
 //   warp 9           MMAs (one thread): S = Q K^T from shared memory, O += P V with P in tensor memory
 //   warps 12-15      8-bit caches: raw tiles (16 KB + scales) to bf16 stages, exact
@@ -44,6 +44,10 @@ constexpr int kHalf = 16 * 1024;               // 128 rows of 64 bf16 values
 constexpr int kStageBytes = 2 * kHalf;         // a K or V tile in bf16
 constexpr int kRawBytes = 16 * 1024;           // the same in 8 bits
 constexpr int kScaleTile = 1024;               // scales of K and V of 128 positions
+#ifndef EXPU
+#define EXPU 4
+#endif
+constexpr int kExpandRows = EXPU;
 #ifndef FMAOF8
 #define FMAOF8 0
 #endif
@@ -305,6 +309,22 @@ struct Stretches {
     }
 };
 
+// The order of an item's K and V tiles in the ring, as the MMAs take them: `ahead` (1 or 2) key tiles, then V 0, K ahead,
+// V 1, ..., and the last V tiles.  Copy k of 2 count: whether it is V, and its tile t; and the reverse.
+__device__ __forceinline__ bool copy_order(int k, int count, int ahead, int& t) {
+    if (ahead == 1) {
+        t = k >> 1;
+        return k & 1;
+    }
+    const bool v = k == 2 * count - 1 || (k > 0 && (k & 1) == 0);
+    t = k == 2 * count - 1 ? count - 1 : v ? k / 2 - 1 : (k + 1) / 2;
+    return v;
+}
+__device__ __forceinline__ int copy_place(bool v, int t, int count, int ahead) {
+    if (ahead == 1) return 2 * t + (v ? 1 : 0);
+    return v ? min(2 * (t + 1), 2 * count - 1) : max(2 * t - 1, 0);
+}
+
 // ---- warp 8: copies -------------------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -314,9 +334,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
         : "memory");
 }
 
+// Warp 8 hands out the stretches and copies q and K, warp 10 copies V (`v`): the issue of 16 page copies takes about
+// half the time that a tile may take, so two warps share it.
 template <int kFmt>
-__device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_t* smem, Walk walk, const CUtensorMap* qm,
-                                          const CUtensorMap* km, const CUtensorMap* vm) {
+__device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8_t* smem, bool v, Walk walk,
+                                           const CUtensorMap* qm, const CUtensorMap* m) {
     using L = Layout<kFmt>;
     const int lane = threadIdx.x & 31;
     constexpr int kRing = L::k8 ? L::kRaw : L::kStages;
@@ -324,45 +346,57 @@ __device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_
     uint64_t* empty = L::k8 ? c.raw_empty : c.kv_empty;
     const uint32_t base = smem_addr(smem);
     const int my = L::k8 ? (lane & 7) : (lane >> 1) & 7;   // the page of the tile that this lane copies
-    uint32_t ring = 0, q_count[2] = {0, 0}, unit_count = 0, segments = 0;
-    Segment s;
-    for (bool more = true; more;) {
-        more = walk.next(s);
-        if (!more) s.j0 = s.j1 = 0;
-        const uint32_t slot = segments % kSegments;
-        pipe_wait(&c.seg_empty[slot], ((segments / kSegments) & 1) ^ 1, &c.dead, a.status);
-        ++segments;
-        if (lane == 0) {
-            c.seg[slot] = s;
-            mbar_arrive(&c.seg_full[slot]);
-        }
-        __syncwarp();
-        if (!more) break;
-        for (int t = 0; t < (s.two ? 2 : 1); ++t) {
-            const bool ok = pipe_wait(&c.q_empty[t], (q_count[t] & 1) ^ 1, &c.dead, a.status);
-            ++q_count[t];
-            if (lane == 0 && ok) {
-                mbar_arrive_expect_tx(&c.q_full[t], (uint32_t)(a.tpt * a.G * kRowBytes));
-                for (int h = 0; h < 2; ++h)
-                    tma_load_3d(base + L::kQ + t * kStageBytes + h * kHalf, qm, h * 64, s.kvh * a.G, s.rows + t * a.tpt,
-                                &c.q_full[t]);
+    uint32_t ring = 0, q_count[2] = {0, 0}, unit = 0, segments = 0;
+    Stretches stretches(c, a.status);
+    while (true) {
+        Segment s;
+        if (!v) {
+            const bool more = walk.next(s);
+            if (!more) s.j0 = s.j1 = 0;
+            const uint32_t slot = segments % kSegments;
+            pipe_wait(&c.seg_empty[slot], ((segments / kSegments) & 1) ^ 1, &c.dead, a.status);
+            ++segments;
+            if (lane == 0) {
+                c.seg[slot] = s;
+                mbar_arrive(&c.seg_full[slot]);
             }
             __syncwarp();
+            if (!more) break;
+            for (int t = 0; t < (s.two ? 2 : 1); ++t) {
+                const bool ok = pipe_wait(&c.q_empty[t], (q_count[t] & 1) ^ 1, &c.dead, a.status);
+                ++q_count[t];
+                if (lane == 0 && ok) {
+                    mbar_arrive_expect_tx(&c.q_full[t], (uint32_t)(a.tpt * a.G * kRowBytes));
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_3d(base + L::kQ + t * kStageBytes + h * kHalf, qm, h * 64, s.kvh * a.G,
+                                    s.rows + t * a.tpt, &c.q_full[t]);
+                }
+                __syncwarp();
+            }
+        } else {
+            const Segment* next = stretches.next();
+            if (next == nullptr) break;
+            s = *next;
+            stretches.done();
         }
-        const int pages = (s.end + kPageSize - 1) / kPageSize, count = s.j1 - s.j0;
+        const int pages = (s.end + kPageSize - 1) / kPageSize, count = s.j1 - s.j0, ahead = s.two ? 1 : 2;
         auto page_of = [&](int t) {   // -1: none there (behind the last position, or a bad entry)
             const int pi = (s.j0 + t) * (kTileRows / kPageSize) + my;
             if (t >= count || pi >= pages) return -1;
             return a.page_table[(long)s.b * a.max_pages + pi];
         };
-        auto load = [&](bool v, int t, int page) {
+        int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2);
+        for (int t = 0; t < count; ++t) {
+            const int page = p0;
+            p0 = p1;
+            p1 = p2;
+            p2 = page_of(t + 3);
             const bool there = (s.j0 + t) * (kTileRows / kPageSize) + my < pages;
             const bool good = there && page >= 0 && page < a.num_pages;
             if (there && !good) report(a.status, SD_ERR_INDEX_OOB);
-            const int st = ring % kRing;
-            const bool ok = pipe_wait(&empty[st], ((ring / kRing) & 1) ^ 1, &c.dead, a.status);
-            ++ring;
-            if (!__all_sync(0xffffffffu, ok)) return;
+            const uint32_t at = ring + copy_place(v, t, count, ahead), st = at % kRing;
+            const bool ok = pipe_wait(&empty[st], ((at / kRing) & 1) ^ 1, &c.dead, a.status);
+            if (!__all_sync(0xffffffffu, ok)) continue;
             uint32_t bytes;
             bool copies;
             if (L::k8) {   // lanes 0-7: elements; lanes 8-15: the scales of both, with K
@@ -376,13 +410,12 @@ __device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_
             if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
             __syncwarp();
             if (copies) {
-                const CUtensorMap* m = v ? vm : km;
                 if (L::k8) {
                     if (lane < 8)
                         tma_load_3d(base + L::kRawOff + st * kRawBytes + my * (kPageSize * kHeadDim), m, 0, s.kvh,
                                     page * kPageSize, &full[st]);
                     else
-                        bulk_copy_g2s(smem + L::kScaleOff + (unit_count % 3) * kScaleTile + my * (kPageSize * 2 * kScaleBytes),
+                        bulk_copy_g2s(smem + L::kScaleOff + ((unit + t) % 3) * kScaleTile + my * (kPageSize * 2 * kScaleBytes),
                                       a.scales + scale_offset(page, s.kvh, 0, a.Hkv), kPageSize * 2 * kScaleBytes, &full[st]);
                 } else {
                     const int h = lane & 1;
@@ -390,21 +423,10 @@ __device__ __forceinline__ void copy_warp(const ChunkArgs& a, Control& c, uint8_
                                 page * kPageSize, &full[st]);
                 }
             }
-            if (!v) ++unit_count;
             __syncwarp();
-        };
-        const int ahead = s.two ? 1 : 2;   // key tiles before the first value tile, as the MMAs take them
-        int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2), p3 = page_of(3);
-        load(false, 0, p0);
-        if (ahead == 2 && count > 1) load(false, 1, p1);
-        for (int t = 0; t < count; ++t) {
-            load(true, t, p0);
-            if (t + ahead < count) load(false, t + ahead, ahead == 1 ? p1 : p2);
-            p0 = p1;
-            p1 = p2;
-            p2 = p3;
-            p3 = page_of(t + 4);
         }
+        ring += 2 * count;
+        unit += count;
     }
     // every copy has landed before the block ends (also after a wait that ran out)
     for (uint32_t x = ring > (uint32_t)kRing ? ring - kRing : 0; x < ring; ++x)
@@ -544,26 +566,32 @@ __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uin
             *reinterpret_cast<uint4*>(line + (((k0 + h) ^ (row & 7)) << 4)) = h ? o1 : o0;
             *reinterpret_cast<uint4*>(line + (((k0 + 1 - h) ^ (row & 7)) << 4)) = h ? o0 : o1;
         };
-        uint32_t by[8];
         bool plain = rows >= kTileRows;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            by[x] = sc[(x * 16 + (tid >> 3)) * (2 * kScaleBytes) + (c16 >> 1)];
-            plain = plain && plain_factor<kFmt>(by[x]);
-        }
-        if (__all_sync(0xffffffffu, plain)) {   // straight-line: the loads and the arithmetic of all rows overlap
+        for (int x = 0; x < 8; ++x)
+            plain = plain && plain_factor<kFmt>(sc[(x * 16 + (tid >> 3)) * (2 * kScaleBytes) + (c16 >> 1)]);
+        if (__all_sync(0xffffffffu, plain)) {   // the loads of four rows, then their arithmetic side by side
+#pragma unroll 1
+            for (int x0 = 0; x0 < 8; x0 += kExpandRows) {
+                uint4 e[kExpandRows];
+                uint32_t f[kExpandRows];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int row = x * 16 + (tid >> 3);
-                const uint4 e = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
-                const uint32_t f = factor_plain<kFmt>(by[x]);
-                uint4 o0, o1;
-                expand4<kFmt>(e.x, o0.x, o0.y);
-                expand4<kFmt>(e.y, o0.z, o0.w);
-                expand4<kFmt>(e.z, o1.x, o1.y);
-                expand4<kFmt>(e.w, o1.z, o1.w);
-                put(row, make_uint4(mul_bf16x2(o0.x, f), mul_bf16x2(o0.y, f), mul_bf16x2(o0.z, f), mul_bf16x2(o0.w, f)),
-                    make_uint4(mul_bf16x2(o1.x, f), mul_bf16x2(o1.y, f), mul_bf16x2(o1.z, f), mul_bf16x2(o1.w, f)));
+                for (int x = 0; x < kExpandRows; ++x) {
+                    const int row = (x0 + x) * 16 + (tid >> 3);
+                    e[x] = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
+                    f[x] = factor_plain<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
+                }
+#pragma unroll
+                for (int x = 0; x < kExpandRows; ++x) {
+                    uint4 o0, o1;
+                    expand4<kFmt>(e[x].x, o0.x, o0.y);
+                    expand4<kFmt>(e[x].y, o0.z, o0.w);
+                    expand4<kFmt>(e[x].z, o1.x, o1.y);
+                    expand4<kFmt>(e[x].w, o1.z, o1.w);
+                    put((x0 + x) * 16 + (tid >> 3),
+                        make_uint4(mul_bf16x2(o0.x, f[x]), mul_bf16x2(o0.y, f[x]), mul_bf16x2(o0.z, f[x]), mul_bf16x2(o0.w, f[x])),
+                        make_uint4(mul_bf16x2(o1.x, f[x]), mul_bf16x2(o1.y, f[x]), mul_bf16x2(o1.z, f[x]), mul_bf16x2(o1.w, f[x])));
+                }
             }
         } else {   // the item's last tile, or a scale at the ends of the range
 #pragma unroll 1
@@ -587,11 +615,10 @@ __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uin
     };
     while (const Segment* s = stretches.next()) {
         const int count = s->j1 - s->j0, ahead = s->two ? 1 : 2, end = s->end - s->j0 * kTileRows;
-        tile(false, end);
-        if (ahead == 2 && count > 1) tile(false, end - kTileRows);
-        for (int t = 0; t < count; ++t) {
-            tile(true, end - t * kTileRows);
-            if (t + ahead < count) tile(false, end - (t + ahead) * kTileRows);
+        for (int k = 0; k < 2 * count; ++k) {   // (one loop body: the code of two would crowd the instruction cache)
+            int t;
+            const bool v = copy_order(k, count, ahead, t);
+            tile(v, end - t * kTileRows);
         }
         stretches.done();
     }
@@ -823,7 +850,7 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
         }
         for (int x = 0; x < kSegments; ++x) {
             mbar_init(&c.seg_full[x], 1);
-            mbar_init(&c.seg_empty[x], L::k8 ? 13 : 9);   // the warps that read them
+            mbar_init(&c.seg_empty[x], L::k8 ? 14 : 10);   // the warps that read them
         }
         mbar_init(&c.done, 1);
         c.dead = 0;
@@ -841,7 +868,7 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
         softmax_warps(a, c);
     } else if (warp < 12) {
         regs_down<L::k8 ? 48 : 72>();
-        if (warp == 8) copy_warp<kFmt>(a, c, smem, Walk(a, c, u0, u1, total), &qm, &km, &vm);
+        if (warp == 8 || warp == 10) copy_warps<kFmt>(a, c, smem, warp == 10, Walk(a, c, u0, u1, total), &qm, warp == 10 ? &vm : &km);
         if (warp == 9) mma_warp<kFmt>(a, c, smem);
     } else if (L::k8) {
         regs_down<64>();

@@ -194,7 +194,10 @@ size_t decode_workspace(const Dims& d, bool dense) {
 }
 
 size_t chunk_workspace() { return chunk_layout().total; }
-size_t cache_sparse_workspace(const Dims&) { return 256; }
+// 8-bit sparse decode: part [2 kCacheSparseWarps][128] fp32, ml [2 kCacheSparseWarps] float2
+size_t cache_sparse_workspace() {
+    return (size_t)2 * kCacheSparseWarps * (kHeadDim * sizeof(float) + sizeof(float2));
+}
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -316,7 +319,7 @@ sd_status sd_workspace_size(const sd_shape* shape, int32_t op, size_t* bytes) {
         case SD_OP_CHUNK: *bytes = chunk_workspace(); return SD_OK;
         case SD_OP_CACHE_SPARSE:
             if (!sparse_fits(d)) return SD_ERR_UNSUPPORTED;
-            *bytes = cache_sparse_workspace(d);
+            *bytes = cache_sparse_workspace();
             return SD_OK;
         default: return SD_ERR_INVALID_ARG;
     }
@@ -744,7 +747,7 @@ sd_status sd_cache_sparse_decode(const sd_shape* shape, const sd_cache* cache, c
         !aligned(lens, 4) || !aligned(idx, 4) || !aligned(dev_status, 4))
         return SD_ERR_INVALID_ARG;
     if (!sparse_fits(d)) return SD_ERR_UNSUPPORTED;
-    if (workspace_bytes < cache_sparse_workspace(d)) return SD_ERR_WORKSPACE;
+    if (workspace_bytes < cache_sparse_workspace()) return SD_ERR_WORKSPACE;
     DeviceInfo di;
     st = device_info(&di);
     if (st != SD_OK) return st;
@@ -757,6 +760,8 @@ sd_status sd_cache_sparse_decode(const sd_shape* shape, const sd_cache* cache, c
     a.lens = lens;
     a.idx = idx;
     a.out = out;
+    a.part = static_cast<float*>(workspace);
+    a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * kCacheSparseWarps * kHeadDim);
     a.status = dev_status;
     a.B = d.B;
     a.Hq = d.Hq;

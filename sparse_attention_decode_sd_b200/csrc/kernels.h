@@ -210,11 +210,16 @@ struct CacheSparseArgs {
     const int32_t* lens;
     const int32_t* idx;
     float* out;
+    // workspace: parts of rows that a share's border cuts, two slots per warp
+    float* part;              // un-normalised outputs [128]
+    float2* ml;               // maximum (log2 units) and sum
     int32_t* status;
     int B, Hq, Hkv, G, max_pages, num_pages, k_max, sms;
+    int shares;               // warps that the slots of idx are cut over
     long n_cap;
     float scale_log2;
 };
+constexpr int kCacheSparseWarps = 4096;   // warps of one wave at most
 cudaError_t launch_cache_sparse(const CacheSparseArgs& a, int format, cudaStream_t stream);
 
 }  // namespace sd

@@ -1,17 +1,32 @@
 // cache_sparse.cu -- exact attention over the selected rows of an 8-bit paged cache (the sparse decode of
 // sparse_decode.cu, for the formats of cache_format.cuh).
 //
-//   out[r] = sum_{i in S_r} w_i V_i / sum_{i in S_r} w_i,  w_i = 2^((q_r . K_i) log2(e) / sqrt(d) - m)
+//   out[r] = sum_{i in S_r} w_i V_i / sum_{i in S_r} w_i,  w_i = 2^(s_i - m),  s_i = (q_r . K_i) log2(e) / sqrt(d)
 //
-// per row r = (request, query head), m the running maximum (kept within 2^8 of it), everything in fp32.
+// per row r = (request, query head).
 //
 // The slots of idx, padding included, are cut evenly over the warps of one wave: no pass over the rows is needed
-// first, full rows (the indexers') balance exactly, and padding costs a read of idx.  Eight lanes take one selected
-// row, 16 dimensions each: 16 bytes of K, 16 of V and the row's 8 scale bytes (the factor of a lane's 16
-// dimensions is one power of two, applied to its share of the score and, for V, to the weight).  A warp keeps four
-// such groups with a maximum, sum and output of their own, joined when the row or the warp's share ends.  Positions
-// are read three steps ahead of their use, page entries two, cache rows one, so that only the gathers' throughput
-// counts.  A row cut by a share's border leaves parts in the workspace; sparse_parts_kernel joins them in order.
+// first, full rows (the indexers') balance exactly, and padding costs a read of idx.  A row cut by a share's border
+// leaves parts in the workspace; sparse_parts_kernel joins them in order.
+//
+// One step of a warp takes 16 selected rows, gathered by 16-byte asynchronous copies into a ring of its own in shared
+// memory (positions are read about six steps ahead of their use, page entries four, cache rows two).  Both products run
+// on the tensor cores (mma.sync m16n8k16) on the 8-bit elements as half-precision values, which hold them exactly;
+// one fp32 dot product per row on the CUDA cores took 50 instructions per selected row, this takes about half.
+//   scores   A = 16 rows of K, B = q with column n holding only block n of it, so that column n of the result is
+//            the dot product over block n, which then takes the block's scale in fp32.  q is scaled by a power of
+//            two to at most 2, which half precision holds to 2^-25 of its largest value.
+//   outputs  A = the weights: row 2 n + i is part i (high, residual: 22 bits) of w_r 2^(e_n(r)), the weight with
+//            the scale of block n folded in, B = V; of the result, block n of the output uses rows 2 n, 2 n + 1.
+//            Each block has a reference M_n of its own (near the largest s + e_n), as scales may span more than
+//            half precision's range; the sum of the weights has the reference m.
+// References lag by up to 2^8 before the accumulators are rescaled.
+//
+// What bounds it: random 128-byte rows.  At 4 x 64 heads x 2621 rows of N = 131072 (168 MB with each row of a group
+// read once) the gathers alone take 52 us for K and V, 4 us more for the scales' 32-byte sectors, and 27-40 us when
+// the same number of rows is read in order; the whole call takes 64 us.
+#include <cuda_fp16.h>
+
 #include "cache_format.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -20,10 +35,26 @@ namespace sd {
 
 namespace {
 
-constexpr int kWarps = 4;          // warps of a CTA (independent of each other)
-constexpr int kPer = 2;            // selected rows per group of eight lanes and step
-constexpr int kStep = 4 * kPer;    // slots of idx per warp and step
-constexpr float kGrow = 8.f;       // log2 units that the maximum may lag behind
+constexpr int kWarps = 1;          // warps of a CTA (independent of each other: one balances the SMs best)
+constexpr int kCtas = 12;          // CTAs per SM (at 13 and more, registers spill and the time grows)
+constexpr int kStep = 16;          // selected rows per warp and step
+constexpr int kDepth = 2;          // steps whose gathers are in flight: one chunk of 32 slots
+constexpr int kRing = kDepth + 1;
+constexpr float kGrow = 8.f;       // log2 units that a reference may lag behind
+constexpr float kLift = 6.f;       // weights are at most about 2^6, with the lag 2^14: clear of half precision's ends
+
+// Rows of one step.  16-byte chunk c of row r lies at chunk c ^ (2 (r & 3)) of K and c ^ (2 ((r >> 1) & 3)) of V: the rows
+// that a fragment load touches at once then fall into different banks.
+struct Step {
+    uint8_t k[kStep][kHeadDim], v[kStep][kHeadDim];
+    uint2 s[kStep];   // scale bytes of K and of V
+};
+constexpr int kSmem = kWarps * kRing * (int)sizeof(Step);
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, bool valid) {   // (zeros where not valid)
+    const int bytes = valid ? 8 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
 // 2^e of a scale byte.  Byte 255 gives an infinity (NaN with the block's zeros).
 template <int kFmt>
@@ -32,43 +63,57 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
     const uint32_t bits = byte > 6u ? (byte - 6u) << 23 : 1u << (byte + 16u);
     return __uint_as_float(byte == 255u ? 0x7f800000u : bits);
 }
-
-// Four elements as fp32, before the scale: e4m3 through the half-precision pair that holds them exactly; int8 as
-// 1024 + (x + 128) in half precision, less 1152.
+// e itself (byte 255: NaN).
 template <int kFmt>
-__device__ __forceinline__ void elements4(uint32_t w, float (&x)[4]) {
-    uint32_t a, b;
-    if (kFmt == kFmtFp8) {
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)w));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
-    } else {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t c = 0x64806480u;   // 1152
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(c));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(c));
-    }
-    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    x[0] = lo.x;
-    x[1] = lo.y;
-    x[2] = hi.x;
-    x[3] = hi.y;
+__device__ __forceinline__ float exponent_of(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)byte - (kFmt == kFmtFp8 ? 127 : 133));
 }
 
-struct Rows {       // one step's gathers of a lane
-    uint4 k[kPer], v[kPer];
-    uint2 s[kPer];
-    uint32_t live;  // bit u: there is a row
-};
+// The elements in the low (hi = 0) or high two bytes of w as a half-precision pair.  int8 as 1024 + (x + 128) less 1152.
+template <int kFmt, int hi>
+__device__ __forceinline__ uint32_t half_pair(uint32_t w) {
+    uint32_t r;
+    if (kFmt == kFmtFp8) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(hi ? w >> 16 : w)));
+    } else {
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w ^ 0x80808080u, 0x64646464u, hi ? 0x4342 : 0x4140)), "r"(0x64806480u));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with zeros in the lower eight rows of A: only the upper rows of the result are kept.
+__device__ __forceinline__ void mma_f16_upper(float (&c)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+    [[maybe_unused]] float x, y;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%8,%5,%8}, {%6,%7}, {%0,%1,%9,%9};\n"
+        : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
+        : "r"(a0), "r"(a2), "r"(b0), "r"(b1), "r"(0u), "f"(0.f));
+}
 
 __device__ __forceinline__ float* part_out(const CacheSparseArgs& a, long slot) { return a.part + slot * kHeadDim; }
 
 template <int kFmt>
-__global__ void __launch_bounds__(kWarps * 32) cache_sparse_kernel(const __grid_constant__ CacheSparseArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const __grid_constant__ CacheSparseArgs a) {
+    extern __shared__ __align__(16) Step ring[];
     pdl_enter();
-    const int lane = threadIdx.x & 31, grp = lane >> 3, c = lane & 7;
+    const int lane = threadIdx.x & 31, grp = lane >> 3, c = lane & 7;   // copies: row within four, 16-byte chunk
+    const int n8 = lane >> 2, kq = lane & 3;                              // fragments: row or column, position
     const long w = (long)blockIdx.x * kWarps + (threadIdx.x >> 5), W = a.shares;
     if (w >= W) return;
+    const uint32_t ring_at = smem_addr(ring + (threadIdx.x >> 5) * kRing), ring_end = ring_at + kDepth * sizeof(Step);
+    // where a lane's chunks of its first row of a step go (of later rows: 4 rows further each time)
+    const uint32_t kdst = grp * kHeadDim + (c ^ (2 * grp)) * 16;
+    const uint32_t vdst0 = offsetof(Step, v) + grp * kHeadDim + (c ^ (2 * (grp >> 1))) * 16;
+    const uint32_t vdst1 = offsetof(Step, v) + grp * kHeadDim + (c ^ (2 * (2 + (grp >> 1)))) * 16;
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.K) + c * 16;
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.V) + c * 16;
     const long total = (long)a.B * a.Hq * a.k_max;
     const long u1 = total * (w + 1) / W;
     for (long u0 = total * w / W; u0 < u1;) {
@@ -80,32 +125,43 @@ __global__ void __launch_bounds__(kWarps * 32) cache_sparse_kernel(const __grid_
         const int32_t* row = a.idx + (long)r * a.k_max;
         const int32_t* table = a.page_table + (long)b * a.max_pages;
 
-        float q[16];
+        // q: lane (n, kq) = (lane / 4, lane % 4), n < 4, holds dimensions 32 n + 8 kq .. + 7, the others zero
+        uint4 qv = make_uint4(0u, 0u, 0u, 0u);
+        if (n8 < 4) qv = reinterpret_cast<const uint4*>(a.q)[(long)r * 16 + n8 * 4 + kq];
+        float q[8] = {bf16_lo(qv.x), bf16_hi(qv.x), bf16_lo(qv.y), bf16_hi(qv.y), bf16_lo(qv.z), bf16_hi(qv.z), bf16_lo(qv.w), bf16_hi(qv.w)};
+        float big = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const uint4 v = reinterpret_cast<const uint4*>(a.q)[(long)r * 16 + c * 2 + x];
-            const uint32_t t[4] = {v.x, v.y, v.z, v.w};
+        for (int x = 0; x < 8; ++x) big = fmaxf(big, fabsf(q[x]));
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                q[x * 8 + y * 2] = bf16_lo(t[y]) * a.scale_log2;
-                q[x * 8 + y * 2 + 1] = bf16_hi(t[y]) * a.scale_log2;
-            }
+        for (int x = 16; x; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+        // the power of two at or below the largest value (of the smallest normal number where that is less)
+        const uint32_t top_bits = max(__float_as_uint(big) & 0x7f800000u, 0x00800000u);
+        const float down = __uint_as_float(0x7f000000u - min(top_bits, 0x7e800000u));
+        const float up = __uint_as_float(min(top_bits, 0x7e800000u)) * a.scale_log2;
+        uint32_t qb[2][2];   // [half of the block][k, k + 8]
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const __half2 v = __floats2half2_rn(q[2 * x] * down, q[2 * x + 1] * down);
+            qb[x >> 1][x & 1] = *reinterpret_cast<const uint32_t*>(&v);
         }
-        float o[16], m = -INFINITY, l = 0.f;
+        float o[4][4][2], M = -INFINITY, m = -INFINITY, l = 0.f;   // [block][tile][column]; M of block n8 / 2
 #pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] = 0.f;
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[x][y][0] = o[x][y][1] = 0.f;
 
-        // lanes 0 .. kStep - 1 look up slot j0 + step * kStep + lane
-        auto position = [&](int step) {
-            const int j = j0 + step * kStep + lane;
-            return lane < kStep && j < j1 ? __ldg(row + j) : -1;
+        // Lookups go by chunks of 32 slots, a lane each (two steps): the entry of idx two chunks ahead of the gathers, the
+        // page-table entry one ahead.
+        auto position = [&](int chunk) {
+            const int j = j0 + chunk * 32 + lane;
+            return j < j1 ? __ldg(row + j) : -1;
         };
-        int before = j0 > 0 ? __ldg(row + j0 - 1) : 0;   // the entry before the step (of the row's first: none)
+        int before = j0 > 0 ? __ldg(row + j0 - 1) : 0;   // the entry before the chunk (of the row's first: none)
         bool first = j0 == 0;
         auto page_of = [&](int& e) {   // also the checks of the entry; e = -1 where nothing is to be read
             int p = __shfl_up_sync(0xffffffffu, e, 1);
             if (lane == 0) p = before;
-            before = __shfl_sync(0xffffffffu, e, kStep - 1);
+            before = __shfl_sync(0xffffffffu, e, 31);
             const bool start = first && lane == 0;
             first = false;
             if (e < 0) return 0;
@@ -116,108 +172,159 @@ __global__ void __launch_bounds__(kWarps * 32) cache_sparse_kernel(const __grid_
             }
             return __ldg(table + e / kPageSize);
         };
-        auto gather = [&](int e, int page) {
-            Rows g;
-            int at = -1;   // page and slot
-            if (e >= 0) {
-                if (page >= 0 && page < a.num_pages) at = page * kPageSize + e % kPageSize;
-                else report(a.status, SD_ERR_INDEX_OOB);
+        auto resolve = [&](int e, int page) {   // page and slot of the entry, or -1
+            if (e < 0) return -1;
+            if (page < 0 || page >= a.num_pages) {
+                report(a.status, SD_ERR_INDEX_OOB);
+                return -1;
             }
-            g.live = 0;
+            return page * kPageSize + e % kPageSize;
+        };
+        auto gather = [&](int at, int half, uint32_t stage) {   // 16 rows of a chunk; rows that are not there become zeros
+            const int mine = at >= 0 ? at * a.Hkv + kvh : -1;   // cache row (below 2^31)
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const int p = __shfl_sync(0xffffffffu, at, u * 4 + grp);
-                g.k[u] = g.v[u] = make_uint4(0u, 0u, 0u, 0u);
-                g.s[u] = make_uint2(0u, 0u);
-                if (p >= 0) {
-                    const long cr = ((long)p * a.Hkv + kvh) * 8 + c;
-                    g.k[u] = __ldg(reinterpret_cast<const uint4*>(a.K) + cr);
-                    g.v[u] = __ldg(reinterpret_cast<const uint4*>(a.V) + cr);
-                    g.s[u] = __ldg(reinterpret_cast<const uint2*>(a.scales + scale_offset(p / kPageSize, kvh, p % kPageSize, a.Hkv)));
-                    g.live |= 1u << u;
-                }
+            for (int u = 0; u < kStep / 4; ++u) {
+                const int i = __shfl_sync(0xffffffffu, mine, half * kStep + u * 4 + grp);
+                const long off = (long)max(i, 0) * kHeadDim;
+                cp_async_16(stage + kdst + u * 4 * kHeadDim, kbase + off, i >= 0);
+                cp_async_16(stage + (u & 1 ? vdst1 : vdst0) + u * 4 * kHeadDim, vbase + off, i >= 0);
             }
-            return g;
+            if ((lane >> 4) == half)
+                cp_async_8(stage + offsetof(Step, s) + (lane & 15) * 8,
+                           a.scales + (at >= 0 ? scale_offset(at / kPageSize, kvh, at % kPageSize, a.Hkv) : 0), at >= 0);
+            cp_async_commit();
         };
 
         const int steps = (j1 - j0 + kStep - 1) / kStep;
         int e0 = position(0), e1 = position(1), e2 = position(2);
         int p0 = page_of(e0), p1 = page_of(e1);
-        Rows cur = gather(e0, p0);
+        int at = resolve(e0, p0);                                     // of the chunk that the gathers are in
+        uint32_t live = __ballot_sync(0xffffffffu, at >= 0), ahead = live;   // of the steps computed, and of that chunk
+        uint32_t fill = ring_at;
+        gather(at, 0, fill);
+        gather(at, 1, fill + sizeof(Step));
+        fill += kDepth * sizeof(Step);
+        uint32_t stage = ring_at;
         for (int t = 0; t < steps; ++t) {
-            const int e3 = position(t + 3);
-            const int p2 = page_of(e2);
-            const Rows nxt = gather(e1, p1);
-            float s[kPer], top = -INFINITY;
+            if ((t & 1) == 0) {   // the gathers reach the next chunk
+                live = ahead;
+                at = resolve(e1, p1);
+                ahead = __ballot_sync(0xffffffffu, at >= 0);
+                p1 = page_of(e2);
+                e1 = e2;
+                e2 = position((t >> 1) + 3);
+            } else {
+                live >>= kStep;
+            }
+            __syncwarp();   // every lane is done with the stage that is filled now
+            gather(at, t & 1, fill);
+            fill = fill == ring_end ? ring_at : fill + (uint32_t)sizeof(Step);
+            cp_async_wait<kDepth>();
+            __syncwarp();
+            const Step& cur = *reinterpret_cast<const Step*>(reinterpret_cast<const uint8_t*>(ring) + (stage - smem_addr(ring)));
+            stage = stage == ring_end ? ring_at : stage + (uint32_t)sizeof(Step);
+
+            // scores: rows n8 and n8 + 8, 8 bytes of each block per lane
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const uint32_t kw[4] = {cur.k[u].x, cur.k[u].y, cur.k[u].z, cur.k[u].w};
-                float d0 = 0.f, d1 = 0.f;
+            for (int x = 0; x < 4; ++x) {
+                const int at = ((2 * x + (kq >> 1)) ^ (2 * (n8 & 3))) * 16 + (kq & 1) * 8;
+                const uint2 w0 = *reinterpret_cast<const uint2*>(&cur.k[n8][at]);
+                const uint2 w1 = *reinterpret_cast<const uint2*>(&cur.k[n8 + 8][at]);
+                const bool on = n8 == x;
+                mma_f16(d, half_pair<kFmt, 0>(w0.x), half_pair<kFmt, 0>(w1.x), half_pair<kFmt, 1>(w0.x),
+                        half_pair<kFmt, 1>(w1.x), on ? qb[0][0] : 0u, on ? qb[0][1] : 0u);
+                mma_f16(d, half_pair<kFmt, 0>(w0.y), half_pair<kFmt, 0>(w1.y), half_pair<kFmt, 1>(w0.y),
+                        half_pair<kFmt, 1>(w1.y), on ? qb[1][0] : 0u, on ? qb[1][1] : 0u);
+            }
+            // columns 2 kq, 2 kq + 1 are blocks (kq < 2): scaled and summed
+            float s0 = 0.f, s1 = 0.f;
+            if (kq < 2) {
+                const uint32_t b0 = cur.s[n8].x >> (16 * kq), b1 = cur.s[n8 + 8].x >> (16 * kq);
+                s0 = fmaf(d[0], scale_of<kFmt>(b0 & 255u), d[1] * scale_of<kFmt>(b0 >> 8 & 255u)) * up;
+                s1 = fmaf(d[2], scale_of<kFmt>(b1 & 255u), d[3] * scale_of<kFmt>(b1 >> 8 & 255u)) * up;
+            }
+            s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+            if (!(live >> n8 & 1)) s0 = -INFINITY;
+            if (!(live >> (n8 + 8) & 1)) s1 = -INFINITY;
+            // rows 2 kq, 2 kq + 1, 2 kq + 8, 2 kq + 9, with the exponents of block n8 / 2
+            float s[4], z[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float k[4];
-                    elements4<kFmt>(kw[x], k);
-                    d0 = fmaf(k[0], q[x * 4], d0);
-                    d1 = fmaf(k[1], q[x * 4 + 1], d1);
-                    d0 = fmaf(k[2], q[x * 4 + 2], d0);
-                    d1 = fmaf(k[3], q[x * 4 + 3], d1);
+            for (int x = 0; x < 4; ++x) {
+                s[x] = __shfl_sync(0xffffffffu, x < 2 ? s0 : s1, (2 * kq + (x & 1)) * 4);
+                const uint32_t byte = cur.s[2 * kq + (x & 1) + 8 * (x >> 1)].y >> (8 * (n8 >> 1)) & 255u;
+                z[x] = s[x] + exponent_of<kFmt>(byte);
+            }
+            const float zt = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), st = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+            if (__any_sync(0xffffffffu, zt - M > kGrow || st - m > kGrow)) {   // (from -infinity: any finite score)
+                float zm = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, 1)), sm = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, 1));
+                zm = fmaxf(M, fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 2)));
+                sm = fmaxf(m, fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, 2)));
+                const float fz = zm > M ? ex2(M - zm) : 1.f, fs = sm > m ? ex2(m - sm) : 1.f;
+                M = zm;
+                m = sm;
+                l *= fs;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        o[x][y][0] *= fz;
+                        o[x][y][1] *= fz;
+                    }
+            }
+            const float ms = m == -INFINITY ? 0.f : m, Ms = M == -INFINITY ? 0.f : M - kLift;
+            uint32_t wa[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                l += ex2(s[2 * x] - ms) + ex2(s[2 * x + 1] - ms);
+                const float w0 = ex2(z[2 * x] - Ms), w1 = ex2(z[2 * x + 1] - Ms);
+                const __half2 hi = __floats2half2_rn(w0, w1);
+                const float2 back = __half22float2(hi);
+                const __half2 lo = __floats2half2_rn(w0 - back.x, w1 - back.y);
+                wa[x] = (n8 & 1) ? *reinterpret_cast<const uint32_t*>(&lo) : *reinterpret_cast<const uint32_t*>(&hi);
+            }
+            // outputs: rows 2 kq, 2 kq + 1 (and + 8), dimensions 32 x + 4 n8 .. + 3 per lane
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int row = 2 * kq + (y & 1) + 8 * (y >> 1);
+                    w[y] = *reinterpret_cast<const uint32_t*>(&cur.v[row][((2 * x + (n8 >> 2)) ^ (2 * kq)) * 16 + (n8 & 3) * 4]);
                 }
-                float d = (d0 + d1) * scale_of<kFmt>(cur.s[u].x >> ((c >> 1) * 8) & 255u);
-                d += __shfl_xor_sync(0xffffffffu, d, 1);
-                d += __shfl_xor_sync(0xffffffffu, d, 2);
-                d += __shfl_xor_sync(0xffffffffu, d, 4);
-                s[u] = (cur.live >> u & 1) ? d : -INFINITY;
-                top = fmaxf(top, s[u]);
+                const uint32_t e0 = __byte_perm(w[0], w[1], 0x5140), e1 = __byte_perm(w[0], w[1], 0x7362);
+                const uint32_t f0 = __byte_perm(w[2], w[3], 0x5140), f1 = __byte_perm(w[2], w[3], 0x7362);
+                mma_f16_upper(o[x][0], wa[0], wa[1], half_pair<kFmt, 0>(e0), half_pair<kFmt, 0>(f0));
+                mma_f16_upper(o[x][1], wa[0], wa[1], half_pair<kFmt, 1>(e0), half_pair<kFmt, 1>(f0));
+                mma_f16_upper(o[x][2], wa[0], wa[1], half_pair<kFmt, 0>(e1), half_pair<kFmt, 0>(f1));
+                mma_f16_upper(o[x][3], wa[0], wa[1], half_pair<kFmt, 1>(e1), half_pair<kFmt, 1>(f1));
             }
-            const bool grow = top - m > kGrow;   // (from -infinity: any finite score)
-            if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? ex2(m - top) : 1.f;
-                if (grow) m = top;
-                l *= f;
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] *= f;
-            }
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const float p = (cur.live >> u & 1) ? ex2(s[u] - m) : 0.f;
-                l += p;
-                const float pv = p * scale_of<kFmt>(cur.s[u].y >> ((c >> 1) * 8) & 255u);
-                const uint32_t vw[4] = {cur.v[u].x, cur.v[u].y, cur.v[u].z, cur.v[u].w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float v[4];
-                    elements4<kFmt>(vw[x], v);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) o[x * 4 + y] = fmaf(pv, v[y], o[x * 4 + y]);
-                }
-            }
-            cur = nxt;
-            e1 = e2;
-            e2 = e3;
-            p1 = p2;
         }
-        // the four groups' parts become one
-        float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        l *= f;
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        cp_async_wait<0>();
+        __syncwarp();
+        // the row's sum over the four lanes of a group; outputs: block n8 / 2, high and residual parts added
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
         const bool whole = j0 == 0 && j1 == a.k_max;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const float f = M == -INFINITY ? 0.f : ex2(M - kLift - m) * inv;
+        float v[8];   // dimensions 32 (n8 / 2) + 8 kq + 0 .. 7
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            o[x] *= f;
-            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 8);
-            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 16);
-            o[x] *= inv;
-        }
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                float x = n8 < 2 ? o[0][y][z] : n8 < 4 ? o[1][y][z] : n8 < 6 ? o[2][y][z] : o[3][y][z];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                v[4 * z + y] = M == -INFINITY ? 0.f : x * f;
+            }
         const long slot = 2 * w + (j0 == 0 ? 1 : 0);   // a share's first row may have begun earlier; its last may go on
-        float4* dst = reinterpret_cast<float4*>(whole ? a.out + (long)r * kHeadDim : part_out(a, slot)) + c * 4;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (grp == x) dst[x] = make_float4(o[x * 4], o[x * 4 + 1], o[x * 4 + 2], o[x * 4 + 3]);
-        if (!whole && lane == 0) a.ml[slot] = make_float2(M, l);
+        float4* dst = reinterpret_cast<float4*>(whole ? a.out + (long)r * kHeadDim : part_out(a, slot)) + (n8 >> 1) * 8 + kq * 2;
+        if ((n8 & 1) == 0) {
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        if (!whole && lane == 0) a.ml[slot] = make_float2(m, l);
     }
 }
 
@@ -232,7 +339,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) sparse_parts_kernel(const __g
     // the share that holds slot x: the w with total w / W <= x < total (w + 1) / W (rounded down)
     const long w0 = ((begin + 1) * W - 1) / total, w1 = ((end + 1) * W - 1) / total;
     if (w0 == w1) return;
-    auto slot_of = [&](long w) { return 2 * w + (total * w / W <= begin ? 1 : 0); };
+    auto slot_of = [&](long w) { return 2 * w + (w == w0 ? 1 : 0); };   // (the row begins in share w0)
     float m = -INFINITY;
     for (long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.ml[slot_of(w)].x);
 #pragma unroll
@@ -258,14 +365,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) sparse_parts_kernel(const __g
 template <int kFmt>
 cudaError_t launch_format(CacheSparseArgs a, cudaStream_t stream) {
     int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, cache_sparse_kernel<kFmt>, kWarps * 32, 0);
+    cudaError_t e = cudaFuncSetAttribute(cache_sparse_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, cache_sparse_kernel<kFmt>, kWarps * 32, kSmem);
     if (e != cudaSuccess) return e;
     const long rows = (long)a.B * a.Hq, slots = rows * a.k_max;
     long shares = (long)a.sms * per_sm * kWarps;
     if (shares > kCacheSparseWarps) shares = kCacheSparseWarps;
-    if (shares > slots) shares = slots;   // (a share without a slot would leave a gap between a row's parts)
+    if (shares > rows) shares -= shares % rows;   // whole numbers of shares to a row: none starts a second row
+    if (shares > slots) shares = slots;           // (a share without a slot would leave a gap between a row's parts)
     a.shares = (int)shares;
-    e = launch_pdl(cache_sparse_kernel<kFmt>, dim3((unsigned)((shares + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, stream, a);
+    e = launch_pdl(cache_sparse_kernel<kFmt>, dim3((unsigned)((shares + kWarps - 1) / kWarps)), dim3(kWarps * 32), kSmem, stream,
+                   a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(sparse_parts_kernel, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, stream,
                    a);

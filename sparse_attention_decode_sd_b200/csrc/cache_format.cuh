@@ -36,32 +36,49 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     return (uint32_t)(min(e, 121) + 133);
 }
 
-// 2^-e for the block's byte (not 255), as two factors whose product is exact at every step (2^133 is beyond fp32).
-template <int kFmt>
-__device__ __forceinline__ void inverse_scale(uint32_t byte, float& f1, float& f2) {
-    const int n = (kFmt == kFmtFp8 ? 127 : 133) - (int)byte;   // -e, within [-121, 133]
-    const int h = n >> 1;
-    f1 = __uint_as_float((uint32_t)(h + 127) << 23);
-    f2 = __uint_as_float((uint32_t)(n - h + 127) << 23);
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Four elements (one byte each, the first in the low byte) of values x * f1 * f2, rounded to nearest, ties
-// to even.
+// Four values (two bf16 pairs) to elements, one byte each, the first in the low byte: the values times 2^-e for the
+// block's byte (not 255), rounded to nearest, ties to even.  The product is exact in bf16 but for results below its
+// range, which round to zero all the same.  (int8: 2^-e is beyond bf16 for the six smallest bytes, and the largest
+// byte's elements may have to saturate: both rare, in a branch.)
 template <int kFmt>
-__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float f1, float f2) {
-    x0 = x0 * f1 * f2;
-    x1 = x1 * f1 * f2;
-    x2 = x2 * f1 * f2;
-    x3 = x3 * f1 * f2;
+__device__ __forceinline__ uint32_t encode4(uint32_t a, uint32_t b, uint32_t byte) {
     if (kFmt == kFmtFp8) {
+        const uint32_t f = (254u - byte) * 0x00800080u;   // 2^(127 - byte)
+        a = mul_bf16x2(a, f);
+        b = mul_bf16x2(b, f);
         uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(bf16_hi(a)), "f"(bf16_lo(a)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(bf16_hi(b)), "f"(bf16_lo(b)));
         return (uint32_t)lo | ((uint32_t)hi << 16);
     }
-    const int i0 = max(-127, min(127, __float2int_rn(x0))), i1 = max(-127, min(127, __float2int_rn(x1)));
-    const int i2 = max(-127, min(127, __float2int_rn(x2))), i3 = max(-127, min(127, __float2int_rn(x3)));
-    return (uint32_t)(i0 & 255) | ((uint32_t)(i1 & 255) << 8) | ((uint32_t)(i2 & 255) << 16) | ((uint32_t)i3 << 24);
+    if (byte < 6u) {
+        a = mul_bf16x2(a, 0x42804280u);   // 2^6, and 2^(127 - byte) below
+        b = mul_bf16x2(b, 0x42804280u);
+        byte += 6u;
+    }
+    const uint32_t f = (260u - byte) * 0x00800080u;   // 2^(133 - byte)
+    a = mul_bf16x2(a, f);
+    b = mul_bf16x2(b, f);
+    float x[4] = {bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b)};
+    if (byte == 254u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmaxf(-127.f, fminf(127.f, x[i]));
+    }
+    uint32_t u[4];   // adding 1.5 * 2^23 rounds to an integer and leaves it in the low byte
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(x[i] + 12582912.f);
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
 }
 
 // The bf16 factors that turn expand4()'s values into the stored ones.  e4m3 elements come out of expand4
@@ -96,17 +113,6 @@ __device__ __forceinline__ bool plain_factor(uint32_t byte) {
 template <int kFmt>
 __device__ __forceinline__ uint32_t factor_plain(uint32_t byte) {
     return (kFmt == kFmtFp8 ? byte + 120u : byte - 6u) * 0x00800080u;
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
 }
 
 // Four elements to two bf16 pairs, before the factor.

@@ -2,37 +2,64 @@
 // 8-bit microscaling formats (cache_format.cuh).
 //
 // Both kernels move each byte once and compute little: they are bound by memory (large batches) or by the
-// latency of one pass (a decode step).  Sixteen lanes take one (row, KV head): 8 values of K and 8 of V per
-// lane, so that a warp's loads and stores are whole 128- or 256-byte rows, and a block of 32 values is four
-// neighbouring lanes, whose largest magnitude takes two shuffles.
+// latency of one pass (a decode step).  The unit of work is a run, the rows of one request in one page, for one KV
+// head: its page is looked up once, and the page's Quest box comes out of the same pass over the rows.  Each CTA
+// counts the runs of every request (a scan over row_start and lens) and takes units in turn.  Sixteen lanes take a
+// unit: 8 values of K and 8 of V per lane and row, so that loads and stores are whole 128- or 256-byte rows, and a
+// block of 32 values is four neighbouring lanes, whose largest magnitude takes two shuffles.  Several rows are
+// loaded before the first one is worked on.
+//
+// B200: 4 x 16384 rows x 8 heads from bf16 to MXFP8 with boxes 94 us (424 MB: 4.5 TB/s; one row per unit and a walk over the
+// page for its box took 383 us, two fp32 factors per value instead of one bf16 product 117 us); 131072 rows x 8 heads
+// of MXFP8 to bf16 139 us (814 MB: 5.8 TB/s); a decode step of 32 requests 8 us.
 #include "cache_format.cuh"
 #include "kernels.h"
-#include "ragged.cuh"
 
 namespace sd {
 
-constexpr int kIoThreads = 256;
+namespace {
 
-__device__ __forceinline__ uint32_t abs_max_bits(const uint4& v) {   // of eight bf16, as fp32 bits
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    return m << 16;
+constexpr int kIoThreads = 256;
+constexpr int kIoCtas = 8;       // CTAs per SM at most (they take units in turn)
+constexpr int kIoWave = 32;      // units per SM up to which runs are split
+constexpr int kWriteRows = 2;    // rows in flight per unit
+constexpr int kReadRows = 8;
+
+// The last b with prefix[b] <= run.
+__device__ __forceinline__ int request_of(const int* prefix, int B, int run) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= run) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
 }
 
-// Eight values of a lane (four lanes are a block): element bytes and the block's scale byte.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The largest magnitude of eight bf16, as bf16 bits (infinities and NaN are the largest).
+__device__ __forceinline__ uint32_t abs_max(const uint4& v) {
+    const uint32_t m = max_u16x2(max_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), max_u16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// Eight values of K and of V of a lane (four lanes are a block): elements and the blocks' scale bytes.
 template <int kFmt>
-__device__ __forceinline__ uint2 quantise8(const uint4& v, uint32_t mask, uint32_t& byte) {
-    uint32_t m = abs_max_bits(v);
-    m = max(m, __shfl_xor_sync(mask, m, 1));
-    m = max(m, __shfl_xor_sync(mask, m, 2));
-    byte = scale_byte<kFmt>(m);
-    if (byte == 255u) return make_uint2(0u, 0u);
-    float f1, f2;
-    inverse_scale<kFmt>(byte, f1, f2);
-    return make_uint2(encode4<kFmt>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), f1, f2),
-                      encode4<kFmt>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), f1, f2));
+__device__ __forceinline__ void quantise8(const uint4& k, const uint4& v, uint32_t mask, uint2& ke, uint2& ve, uint32_t& kb,
+                                          uint32_t& vb) {
+    uint32_t m = abs_max(k) | (abs_max(v) << 16);
+    m = max_u16x2(m, __shfl_xor_sync(mask, m, 1));
+    m = max_u16x2(m, __shfl_xor_sync(mask, m, 2));
+    kb = scale_byte<kFmt>(m << 16);
+    vb = scale_byte<kFmt>(m & 0xffff0000u);
+    ke = make_uint2(encode4<kFmt>(k.x, k.y, kb), encode4<kFmt>(k.z, k.w, kb));
+    ve = make_uint2(encode4<kFmt>(v.x, v.y, vb), encode4<kFmt>(v.z, v.w, vb));
+    if (kb == 255u) ke = make_uint2(0u, 0u);
+    if (vb == 255u) ve = make_uint2(0u, 0u);
 }
 
 template <int kFmt>
@@ -58,70 +85,146 @@ __device__ __forceinline__ void box_with(uint4& lo, uint4& hi, const uint4& v) {
     }
 }
 
-// New rows into the cache.  The first new row of each page also makes the page's Quest box: the minimum and
-// maximum, as stored, of the page's new rows and -- when rows were there before -- of the stored box.
+// The runs of the batch: `prefix` (shared memory, [B + 1]) gets the number of runs before each request.  Request b's
+// rows are positions begin(b, n, N) .. + n - 1; a bad request is reported and has none.  Returns the number of runs, 0
+// where row_start is not valid.
+struct Rows {
+    int rs, begin, n;   // first row, its position, rows
+};
+template <bool kRead>
+__device__ __forceinline__ Rows rows_of(const CacheIoArgs& a, int b) {
+    Rows r;
+    r.rs = a.row_start[b];
+    r.n = a.row_start[b + 1] - r.rs;
+    r.begin = kRead ? a.first[b] : a.lens[b] - r.n;
+    return r;
+}
+template <bool kRead>
+__device__ __forceinline__ int plan_runs(const CacheIoArgs& a, int* prefix, int* scratch) {
+    const int per = (a.B + kIoThreads - 1) / kIoThreads;
+    const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    bool bad = false;
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int lo = a.row_start[b], hi = a.row_start[b + 1];
+        bad = bad || lo < 0 || hi < lo || hi > a.total_rows;
+        const int N = a.lens[b], n = hi - lo;
+        if (bad || n == 0) continue;
+        const int begin = kRead ? a.first[b] : N - n;
+        if (N < 0 || (long)N > a.n_cap || begin < 0 || (long)begin + n > N) {
+            if (blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
+            continue;
+        }
+        mine += (begin + n - 1) / kPageSize - begin / kPageSize + 1;
+    }
+    if (__syncthreads_or(bad ? 1 : 0)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
+        return 0;
+    }
+    int total;
+    int at = block_exclusive_scan(mine, scratch, &total);
+    for (int b = b0; b < b1; ++b) {
+        prefix[b] = at;
+        const Rows r = rows_of<kRead>(a, b);
+        const int N = a.lens[b];
+        if (r.n > 0 && N >= 0 && (long)N <= a.n_cap && r.begin >= 0 && (long)r.begin + r.n <= N)
+            at += (r.begin + r.n - 1) / kPageSize - r.begin / kPageSize + 1;
+    }
+    if (threadIdx.x == 0) prefix[a.B] = total;
+    __syncthreads();
+    return total;
+}
+
+// Part `part` of run `run`: the rows whose slots lie in its share of the page.  page -1: a bad entry, reported.
+struct Run {
+    int page, slot, row, count;
+    bool joins;   // the page holds earlier rows of the request
+};
+template <bool kRead>
+__device__ __forceinline__ Run run_of(const CacheIoArgs& a, const int* prefix, int run, int slot0, int slot1) {
+    const int b = request_of(prefix, a.B, run);   // (requests without runs share their successor's prefix)
+    const Rows r = rows_of<kRead>(a, b);
+    const int pi = r.begin / kPageSize + run - prefix[b];
+    const int p0 = max(r.begin, pi * kPageSize + slot0), p1 = min(r.begin + r.n, pi * kPageSize + slot1);
+    Run u;
+    u.page = a.page_table[(long)b * a.max_pages + pi];
+    u.slot = p0 - pi * kPageSize;
+    u.row = r.rs + p0 - r.begin;
+    u.count = p1 - p0;
+    u.joins = r.begin > pi * kPageSize;
+    if (u.page < 0 || u.page >= a.num_pages) {
+        report(a.status, SD_ERR_INDEX_OOB);
+        u.count = 0;
+    }
+    return u;
+}
+
+// New rows into the cache, and the Quest box of each run's page: the minimum and maximum, as stored, of its rows and
+// -- where the request had rows there before -- of the stored box.  Where runs are taken in parts, one more unit per run
+// makes the box alone (from the new rows, rounded again).
 template <int kFmt>
-__global__ void __launch_bounds__(kIoThreads) cache_write_kernel(CacheIoArgs a) {
-    extern __shared__ int rs[];
+__global__ void __launch_bounds__(kIoThreads, 4) cache_write_kernel(const __grid_constant__ CacheIoArgs a) {
+    extern __shared__ int prefix[];
+    __shared__ int scratch[40];
     pdl_enter();
-    if (!load_row_start(a.row_start, a.B, a.total_rows, rs, a.status)) return;
+    const bool apart = a.parts > 1 && a.boxes != nullptr;   // boxes by units of their own
+    const int per_run = a.parts + (apart ? 1 : 0), share = kPageSize / a.parts;
+    const long units = (long)plan_runs<false>(a, prefix, scratch) * per_run * a.Hkv;
     const int c = threadIdx.x & 15;
     const uint32_t mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
-    const long per_grid = (long)gridDim.x * (kIoThreads / 16);
-    const long first = (long)rs[0] * a.Hkv, items = (long)rs[a.B] * a.Hkv;
-    for (long it = first + (long)blockIdx.x * (kIoThreads / 16) + (threadIdx.x >> 4); it < items; it += per_grid) {
-        const int t = (int)(it / a.Hkv), kvh = (int)(it - (long)t * a.Hkv);
-        const long src = it * 16 + c;
-        const uint4 kr = reinterpret_cast<const uint4*>(a.k_in)[src];
-        const uint4 vr = reinterpret_cast<const uint4*>(a.v_in)[src];
-        const int b = request_of(rs, a.B, t);
-        const int n = rs[b + 1] - rs[b], N = checked_len(a.lens, b, a.n_cap, a.status);
-        if (n > N) {
-            report(a.status, SD_ERR_INVALID_ARG);
-            continue;
+    for (long it = (long)blockIdx.x * (kIoThreads / 16) + (threadIdx.x >> 4); it < units; it += (long)gridDim.x * (kIoThreads / 16)) {
+        const int x = (int)(it / a.Hkv), kvh = (int)(it - (long)x * a.Hkv), run = x / per_run, part = x - run * per_run;
+        const bool alone = part == a.parts;
+        const Run u = run_of<false>(a, prefix, run, alone ? 0 : part * share, alone ? kPageSize : (part + 1) * share);
+        if (u.count <= 0) continue;
+        const long src = ((long)u.row * a.Hkv + kvh) * 16 + c;                                    // 16-byte chunks
+        const long dst = (((long)u.page * kPageSize + u.slot) * a.Hkv + kvh) * 16 + c;            // 16- or 8-byte chunks
+        const long step = (long)a.Hkv * 16;
+        uint4* box = a.boxes == nullptr || apart != alone ? nullptr
+                                                          : reinterpret_cast<uint4*>(a.boxes) + ((long)u.page * a.Hkv + kvh) * 32 + c;
+        uint4 lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);   // +inf, -inf
+        uint4 hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        if (box != nullptr && u.joins) {
+            lo = box[0];
+            hi = box[16];
         }
-        const int p = N - n + (t - rs[b]);
-        const int page = a.page_table[(long)b * a.max_pages + p / kPageSize];
-        if (page < 0 || page >= a.num_pages) {
-            report(a.status, SD_ERR_INDEX_OOB);
-            continue;
-        }
-        const int slot = p % kPageSize;
-        const long row = ((long)page * kPageSize + slot) * a.Hkv + kvh;
-        uint4 kept = kr;
-        if (kFmt == kFmtBf16) {
-            reinterpret_cast<uint4*>(a.K)[row * 16 + c] = kr;
-            reinterpret_cast<uint4*>(a.V)[row * 16 + c] = vr;
-        } else {
-            uint32_t kb, vb;
-            const uint2 ke = quantise8<kFmt>(kr, mask, kb), ve = quantise8<kFmt>(vr, mask, vb);
-            reinterpret_cast<uint2*>(a.K)[row * 16 + c] = ke;
-            reinterpret_cast<uint2*>(a.V)[row * 16 + c] = ve;
-            if ((c & 3) == 0) {
-                uint8_t* s = a.scales + scale_offset(page, kvh, slot, a.Hkv) + (c >> 2);
-                s[0] = (uint8_t)kb;
-                s[kScaleBytes] = (uint8_t)vb;
-            }
-            kept = dequantise8<kFmt>(ke, kb);
-        }
-        if (a.boxes != nullptr && (slot == 0 || t == rs[b])) {
-            uint4* box = reinterpret_cast<uint4*>(a.boxes) + ((long)page * a.Hkv + kvh) * 32 + c;
-            uint4 lo = kept, hi = kept;
-            if (slot != 0) {
-                lo = box[0];
-                hi = box[16];
-                box_with(lo, hi, kept);
-            }
-            const int more = min(kPageSize - slot, rs[b + 1] - t);
-            for (int j = 1; j < more; ++j) {
-                uint4 r = reinterpret_cast<const uint4*>(a.k_in)[src + (long)j * a.Hkv * 16];
-                if (kFmt != kFmtBf16) {
-                    uint32_t kb;
-                    const uint2 ke = quantise8<kFmt>(r, mask, kb);
-                    r = dequantise8<kFmt>(ke, kb);
+        for (int j0 = 0; j0 < u.count; j0 += kWriteRows) {
+            uint4 k[kWriteRows], v[kWriteRows];
+#pragma unroll
+            for (int j = 0; j < kWriteRows; ++j)
+                if (j0 + j < u.count) {
+                    k[j] = __ldg(reinterpret_cast<const uint4*>(a.k_in) + src + (j0 + j) * step);
+                    v[j] = __ldg(reinterpret_cast<const uint4*>(a.v_in) + src + (j0 + j) * step);
                 }
-                box_with(lo, hi, r);
+#pragma unroll
+            for (int j = 0; j < kWriteRows; ++j) {
+                if (j0 + j >= u.count) continue;
+                const long to = dst + (j0 + j) * step;
+                if (kFmt == kFmtBf16) {
+                    if (!alone) {
+                        reinterpret_cast<uint4*>(a.K)[to] = k[j];
+                        reinterpret_cast<uint4*>(a.V)[to] = v[j];
+                    }
+                } else {
+                    uint32_t kb, vb;
+                    uint2 ke, ve;
+                    quantise8<kFmt>(k[j], v[j], mask, ke, ve, kb, vb);
+                    if (!alone) {
+                        reinterpret_cast<uint2*>(a.K)[to] = ke;
+                        reinterpret_cast<uint2*>(a.V)[to] = ve;
+                        uint32_t s = kb | vb << 8, t = __shfl_xor_sync(mask, s, 4);   // the row's bytes together
+                        s = (c & 4) ? t | s << 16 : s | t << 16;
+                        t = __shfl_xor_sync(mask, s, 8);
+                        if (c == 0)
+                            *reinterpret_cast<uint2*>(a.scales + scale_offset(u.page, kvh, u.slot + j0 + j, a.Hkv)) =
+                                make_uint2(__byte_perm(s, t, 0x6420), __byte_perm(s, t, 0x7531));
+                    }
+                    if (box != nullptr) k[j] = dequantise8<kFmt>(ke, kb);
+                }
+                if (box != nullptr) box_with(lo, hi, k[j]);
             }
+        }
+        if (box != nullptr) {
             box[0] = lo;
             box[16] = hi;
         }
@@ -130,52 +233,63 @@ __global__ void __launch_bounds__(kIoThreads) cache_write_kernel(CacheIoArgs a) 
 
 // Positions first[b] .. first[b] + n_b - 1 of every request back as bf16 rows.
 template <int kFmt>
-__global__ void __launch_bounds__(kIoThreads) cache_read_kernel(CacheIoArgs a) {
-    extern __shared__ int rs[];
+__global__ void __launch_bounds__(kIoThreads, 3) cache_read_kernel(const __grid_constant__ CacheIoArgs a) {
+    extern __shared__ int prefix[];
+    __shared__ int scratch[40];
     pdl_enter();
-    if (!load_row_start(a.row_start, a.B, a.total_rows, rs, a.status)) return;
+    const int share = kPageSize / a.parts;
+    const long units = (long)plan_runs<true>(a, prefix, scratch) * a.parts * a.Hkv;
     const int c = threadIdx.x & 15;
-    const long per_grid = (long)gridDim.x * (kIoThreads / 16);
-    const long first = (long)rs[0] * a.Hkv, items = (long)rs[a.B] * a.Hkv;
-    for (long it = first + (long)blockIdx.x * (kIoThreads / 16) + (threadIdx.x >> 4); it < items; it += per_grid) {
-        const int t = (int)(it / a.Hkv), kvh = (int)(it - (long)t * a.Hkv);
-        const int b = request_of(rs, a.B, t);
-        const int n = rs[b + 1] - rs[b], N = checked_len(a.lens, b, a.n_cap, a.status), p0 = a.first[b];
-        if (p0 < 0 || (long)p0 + n > N) {
-            report(a.status, SD_ERR_INVALID_ARG);
-            continue;
-        }
-        const int p = p0 + (t - rs[b]);
-        const int page = a.page_table[(long)b * a.max_pages + p / kPageSize];
-        if (page < 0 || page >= a.num_pages) {
-            report(a.status, SD_ERR_INDEX_OOB);
-            continue;
-        }
-        const int slot = p % kPageSize;
-        const long row = ((long)page * kPageSize + slot) * a.Hkv + kvh;
-        const long dst = it * 16 + c;
-        const uint8_t* s = kFmt == kFmtBf16 ? nullptr : a.scales + scale_offset(page, kvh, slot, a.Hkv) + (c >> 2);
-        if (a.k_out != nullptr) {
-            const uint4 r = kFmt == kFmtBf16 ? reinterpret_cast<const uint4*>(a.K)[row * 16 + c]
-                                             : dequantise8<kFmt>(reinterpret_cast<const uint2*>(a.K)[row * 16 + c], s[0]);
-            reinterpret_cast<uint4*>(a.k_out)[dst] = r;
-        }
-        if (a.v_out != nullptr) {
-            const uint4 r = kFmt == kFmtBf16
-                                ? reinterpret_cast<const uint4*>(a.V)[row * 16 + c]
-                                : dequantise8<kFmt>(reinterpret_cast<const uint2*>(a.V)[row * 16 + c], s[kScaleBytes]);
-            reinterpret_cast<uint4*>(a.v_out)[dst] = r;
+    for (long it = (long)blockIdx.x * (kIoThreads / 16) + (threadIdx.x >> 4); it < units; it += (long)gridDim.x * (kIoThreads / 16)) {
+        const int x = (int)(it / a.Hkv), kvh = (int)(it - (long)x * a.Hkv), run = x / a.parts, part = x - run * a.parts;
+        const Run u = run_of<true>(a, prefix, run, part * share, (part + 1) * share);
+        if (u.count <= 0) continue;
+        const long src = (((long)u.page * kPageSize + u.slot) * a.Hkv + kvh) * 16 + c;
+        const long dst = ((long)u.row * a.Hkv + kvh) * 16 + c;
+        const long step = (long)a.Hkv * 16;
+        const uint8_t* sc = kFmt == kFmtBf16 ? nullptr : a.scales + scale_offset(u.page, kvh, u.slot, a.Hkv) + (c >> 2);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // K, V
+            const void* from = half ? a.V : a.K;
+            uint4* to = reinterpret_cast<uint4*>(half ? a.v_out : a.k_out);
+            if (to == nullptr) continue;
+            for (int j0 = 0; j0 < u.count; j0 += kReadRows) {
+                uint4 r[kReadRows];
+                uint2 e[kReadRows];
+                uint32_t by[kReadRows];
+#pragma unroll
+                for (int j = 0; j < kReadRows; ++j)
+                    if (j0 + j < u.count) {
+                        if (kFmt == kFmtBf16) {
+                            r[j] = __ldg(reinterpret_cast<const uint4*>(from) + src + (j0 + j) * step);
+                        } else {
+                            e[j] = __ldg(reinterpret_cast<const uint2*>(from) + src + (j0 + j) * step);
+                            by[j] = __ldg(sc + (j0 + j) * 2 * kScaleBytes + half * kScaleBytes);
+                        }
+                    }
+#pragma unroll
+                for (int j = 0; j < kReadRows; ++j)
+                    if (j0 + j < u.count) to[dst + (j0 + j) * step] = kFmt == kFmtBf16 ? r[j] : dequantise8<kFmt>(e[j], by[j]);
+            }
         }
     }
 }
 
-static cudaError_t launch_io(void (*kernel)(CacheIoArgs), const CacheIoArgs& a, cudaStream_t stream) {
-    const long want = ((long)a.total_rows * a.Hkv + kIoThreads / 16 - 1) / (kIoThreads / 16);
-    const long most = (long)a.sms * 8;
+template <typename Kernel>
+cudaError_t launch_io(Kernel kernel, CacheIoArgs a, cudaStream_t stream) {
+    // at most total_rows / 16 + 2 B runs (and no more than rows)
+    const long runs = min((long)a.total_rows, (long)a.total_rows / kPageSize + 2L * a.B);
+    // Small batches take runs in parts, so that every SM has work: as many as keep the units within about one wave.
+    a.parts = 1;
+    while (a.parts < kPageSize && runs * a.Hkv * a.parts * 2 <= (long)a.sms * kIoWave) a.parts *= 2;
+    const long units = runs * a.Hkv * (a.parts + (a.parts > 1 && a.boxes != nullptr ? 1 : 0));
+    const long want = (units + kIoThreads / 16 - 1) / (kIoThreads / 16), most = (long)a.sms * kIoCtas;
     const unsigned grid = (unsigned)(want < 1 ? 1 : want < most ? want : most);
     cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kIoThreads), sizeof(int) * (a.B + 1), stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t launch_cache_write(const CacheIoArgs& a, int format, cudaStream_t stream) {
     return launch_io(format == kFmtBf16 ? cache_write_kernel<kFmtBf16>

@@ -39,7 +39,6 @@
 
 #include "cache_format.cuh"
 #include "kernels.h"
-#include "ragged.cuh"
 #include "tcgen05.cuh"
 
 namespace sd {

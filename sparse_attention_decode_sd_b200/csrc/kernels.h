@@ -168,6 +168,7 @@ struct CacheIoArgs {
     __nv_bfloat16* boxes;     // write: Quest boxes of the written pages, or null
     int32_t* status;
     int B, Hkv, max_pages, num_pages, total_rows, sms;
+    int parts;                // units that a run of rows in one page is taken in
     long n_cap;
 };
 cudaError_t launch_cache_write(const CacheIoArgs& a, int format, cudaStream_t stream);

@@ -122,9 +122,9 @@ __device__ __forceinline__ uint32_t factor_plain(uint32_t byte) {
 template <int kFmt>
 __device__ __forceinline__ void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if (kFmt == kFmtFp8) {
-        const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-        lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-        hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+        const uint32_t a = __byte_perm(w, 0u, 0x4140), b = __byte_perm(w, 0u, 0x4342);   // the bytes in the low halves
+        lo = a * 16u + (a & 0x00800080u) * 240u;   // up by 4, the sign by 8 (multiplications: the shifter is the busier pipe)
+        hi = b * 16u + (b & 0x00800080u) * 240u;
     } else {
         const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
         lo = sub_bf16x2(a & 0xff7fff7fu, a & 0xff80ff80u);

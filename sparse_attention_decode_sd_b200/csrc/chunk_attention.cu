@@ -17,7 +17,7 @@
 //   warps 8, 10      copies: K and V page by page (one TMA box of 16 rows x 64 values per page and half, in
 //                    the 128-byte swizzle, into a ring of 32 KB stages), the two tiles of q
 //   warp 9           MMAs (one thread): S = Q K^T from shared memory, O += P V with P in tensor memory
-//   warps 12-15      8-bit caches: raw tiles (16 KB + scales) to bf16 stages, exact
+//   warps 12-19      8-bit caches: raw tiles (16 KB + scales) to bf16 stages, exact
 // While one tile's warps take the softmax of a unit, the tensor cores work on the other tile: per unit
 // P0 V, Q0 K', P1 V, Q1 K' (K' the next unit's keys), so both are busy in turn.  P (bf16) overwrites the first
 // half of its scores.
@@ -50,22 +50,21 @@ constexpr int kHalf = 16 * 1024;               // 128 rows of 64 bf16 values
 constexpr int kStageBytes = 2 * kHalf;         // a K or V tile in bf16
 constexpr int kRawBytes = 16 * 1024;           // the same in 8 bits
 constexpr int kScaleTile = 1024;               // scales of K and V of 128 positions
-constexpr int kExpandRows = 4;                 // rows of an 8-bit tile that a thread expands side by side
-constexpr int kFmaOf8 = 2;                     // of eight pairs of weights, those computed on the FMA pipe
+constexpr int kExpandThreads = 256;            // that expand 8-bit tiles (half of them take twice as long: latency)
 constexpr float kFarAbove = 16384.f;            // sum of a tile's weights from which its row takes a new reference
 
 template <int kFmt>
 struct Layout {
     static constexpr bool k8 = kFmt != kFmtBf16;
     static constexpr int kStages = k8 ? 3 : 5;
-    static constexpr int kRaw = k8 ? 3 : 0;
-    static constexpr int kScaleSlots = k8 ? 3 : 0;
+    static constexpr int kRaw = k8 ? 3 : 1;
+    static constexpr int kScaleSlots = k8 ? 3 : 1;   // (K tile t + 3 is copied only after V tile t is expanded)
     static constexpr int kQ = 0;
     static constexpr int kKv = 2 * kStageBytes;
     static constexpr int kRawOff = kKv + kStages * kStageBytes;
-    static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
-    static constexpr int kCtl = kScaleOff + kScaleSlots * kScaleTile;
-    static constexpr int kThreads = k8 ? 512 : 384;
+    static constexpr int kScaleOff = kRawOff + (k8 ? kRaw * kRawBytes : 0);
+    static constexpr int kCtl = kScaleOff + (k8 ? kScaleSlots * kScaleTile : 0);
+    static constexpr int kThreads = k8 ? 640 : 384;
 };
 
 constexpr int kSegments = 4;   // stretches that the copies may run ahead
@@ -94,7 +93,7 @@ struct Control {
     uint32_t tmem;
     int dead;                // a wait ran out: nothing more is issued
     int b, kvh, pair, unit;  // where this CTA's share starts
-    long long scan[16];
+    long long scan[20];
     float2 post[2 * kTileRows];   // maximum and sum of the two sides of a one-tile item
 };
 
@@ -104,23 +103,30 @@ constexpr int chunk_smem() {
 }
 static_assert(chunk_smem<kFmtBf16>() <= 227 * 1024 && chunk_smem<kFmtFp8>() <= 227 * 1024, "shared memory");
 
-// A bounded wait; once one has run out, every later one gives up soon.  (The timer and the flag are looked at now
-// and then: reading them in every round costs latency.)
-__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = 0;
-    for (uint32_t it = 0; it < kWaitLimitIters; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 31) == 31) {
-            if (*reinterpret_cast<volatile int*>(dead)) return false;
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) break;
+// A bounded wait of a converged warp; false for the whole warp once this or any other wait of the block has run out.
+// The caller then leaves its role without another arrival or copy: a barrier that others still use gets no arrival that
+// they do not expect.  (The timer and the flag are looked at now and then: reading them in every round costs latency.)
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* status, uint64_t* also = nullptr,
+                                          uint32_t also_parity = 0) {
+    auto there = [&]() { return mbar_try_wait(bar, parity) && (also == nullptr || mbar_try_wait(also, also_parity)); };
+    bool ok = there();
+    if (!ok) {
+        uint64_t t0 = 0;
+        for (uint32_t it = 0; it < kWaitLimitIters && !ok; ++it) {
+            ok = there();
+            if (!ok && (it & 31) == 31) {
+                if (*reinterpret_cast<volatile int*>(dead)) break;
+                const uint64_t now = global_timer_ns();
+                if (t0 == 0) t0 = now;
+                if (now - t0 > kWaitLimitNs) break;
+            }
+        }
+        if (!ok && *reinterpret_cast<volatile int*>(dead) == 0) {
+            *reinterpret_cast<volatile int*>(dead) = 1;
+            report(status, SD_ERR_TIMEOUT);
         }
     }
-    *reinterpret_cast<volatile int*>(dead) = 1;
-    report(status, SD_ERR_TIMEOUT);
-    return false;
+    return __all_sync(0xffffffffu, ok);
 }
 
 // ---- the batch as units --------------------------------------------------------------------------------
@@ -297,10 +303,8 @@ struct Stretches {
     __device__ Stretches(Control& control, int32_t* st) : c(control), status(st), n(0) {}
     __device__ __forceinline__ const Segment* next() {   // null: no more
         const uint32_t slot = n % kSegments;
-        bool ok = pipe_wait(&c.seg_full[slot], (n / kSegments) & 1, &c.dead, status);
-        ok = __all_sync(0xffffffffu, ok);
         const Segment* s = &c.seg[slot];
-        return ok && s->j1 > s->j0 ? s : nullptr;
+        return pipe_wait(&c.seg_full[slot], (n / kSegments) & 1, &c.dead, status) && s->j1 > s->j0 ? s : nullptr;
     }
     __device__ __forceinline__ void done() {
         __syncwarp();
@@ -348,13 +352,15 @@ __device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8
     const int my = L::k8 ? (lane & 7) : (lane >> 1) & 7;   // the page of the tile that this lane copies
     uint32_t ring = 0, q_count[2] = {0, 0}, unit = 0, segments = 0;
     Stretches stretches(c, a.status);
-    while (true) {
+    bool ok = true;
+    while (ok) {
         Segment s;
         if (!v) {
             const bool more = walk.next(s);
             if (!more) s.j0 = s.j1 = 0;
             const uint32_t slot = segments % kSegments;
-            pipe_wait(&c.seg_empty[slot], ((segments / kSegments) & 1) ^ 1, &c.dead, a.status);
+            ok = pipe_wait(&c.seg_empty[slot], ((segments / kSegments) & 1) ^ 1, &c.dead, a.status);
+            if (!ok) break;
             ++segments;
             if (lane == 0) {
                 c.seg[slot] = s;
@@ -363,7 +369,7 @@ __device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8
             __syncwarp();
             if (!more) break;
             for (int t = 0; t < (s.two ? 2 : 1); ++t) {
-                const bool ok = pipe_wait(&c.q_empty[t], (q_count[t] & 1) ^ 1, &c.dead, a.status);
+                ok = ok && pipe_wait(&c.q_empty[t], (q_count[t] & 1) ^ 1, &c.dead, a.status);
                 ++q_count[t];
                 if (lane == 0 && ok) {
                     mbar_arrive_expect_tx(&c.q_full[t], (uint32_t)(a.tpt * a.G * kRowBytes));
@@ -386,7 +392,7 @@ __device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8
             return a.page_table[(long)s.b * a.max_pages + pi];
         };
         int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2);
-        for (int t = 0; t < count; ++t) {
+        for (int t = 0; t < count && ok; ++t) {
             const int page = p0;
             p0 = p1;
             p1 = p2;
@@ -395,8 +401,8 @@ __device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8
             const bool good = there && page >= 0 && page < a.num_pages;
             if (there && !good) report(a.status, SD_ERR_INDEX_OOB);
             const uint32_t at = ring + copy_place(v, t, count, ahead), st = at % kRing;
-            const bool ok = pipe_wait(&empty[st], ((at / kRing) & 1) ^ 1, &c.dead, a.status);
-            if (!__all_sync(0xffffffffu, ok)) continue;
+            ok = pipe_wait(&empty[st], ((at / kRing) & 1) ^ 1, &c.dead, a.status);
+            if (!ok) break;
             uint32_t bytes;
             bool copies;
             if (L::k8) {   // lanes 0-7: elements; lanes 8-15: the scales of both, with K
@@ -415,7 +421,7 @@ __device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8
                         tma_load_3d(base + L::kRawOff + st * kRawBytes + my * (kPageSize * kHeadDim), m, 0, s.kvh,
                                     page * kPageSize, &full[st]);
                     else
-                        bulk_copy_g2s(smem + L::kScaleOff + ((unit + t) % 3) * kScaleTile + my * (kPageSize * 2 * kScaleBytes),
+                        bulk_copy_g2s(smem + L::kScaleOff + ((unit + t) % L::kScaleSlots) * kScaleTile + my * (kPageSize * 2 * kScaleBytes),
                                       a.scales + scale_offset(page, s.kvh, 0, a.Hkv), kPageSize * 2 * kScaleBytes, &full[st]);
                 } else {
                     const int h = lane & 1;
@@ -428,10 +434,10 @@ __device__ __forceinline__ void copy_warps(const ChunkArgs& a, Control& c, uint8
         ring += 2 * count;
         unit += count;
     }
-    // every copy has landed before the block ends (also after a wait that ran out)
-    for (uint32_t x = ring > (uint32_t)kRing ? ring - kRing : 0; x < ring; ++x)
-        if (!c.dead) mbar_wait(&full[x % kRing], (x / kRing) & 1);
-    if (c.dead) {
+    // every copy has landed before the block ends; after a wait that ran out, which ones are under way is not known
+    for (uint32_t x = ring > (uint32_t)kRing ? ring - kRing : 0; x < ring && ok; ++x)
+        ok = pipe_wait(&full[x % kRing], (x / kRing) & 1, &c.dead, a.status);
+    if (!ok) {
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000ull) {
         }
@@ -448,14 +454,15 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
     uint32_t ring = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
     Stretches stretches(c, a.status);
 
+    bool ok = true;   // else nothing more is issued
     auto wait_stage = [&]() -> uint32_t {   // the next stage of the ring, full
         const uint32_t st = ring % L::kStages;
-        pipe_wait(&c.kv_full[st], (ring / L::kStages) & 1, &c.dead, a.status);
+        ok = ok && pipe_wait(&c.kv_full[st], (ring / L::kStages) & 1, &c.dead, a.status);
         ++ring;
-        __syncwarp();
         return st;
     };
     auto qk = [&](int g, int tile, uint32_t st) {
+        if (!ok) return;
         const uint32_t qd = smem_desc(base + L::kQ + tile * kStageBytes, 16);
         const uint32_t kd = smem_desc(base + L::kKv + st * kStageBytes, 16);
 #pragma unroll
@@ -467,17 +474,20 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
     };
     auto pv = [&](int g, uint32_t st, bool add) {
         const uint32_t vd = smem_desc(base + L::kKv + st * kStageBytes, kHalf);
-        pipe_wait(&c.p_full[g], p_count[g] & 1, &c.dead, a.status);
+        ok = ok && pipe_wait(&c.p_full[g], p_count[g] & 1, &c.dead, a.status);
         ++p_count[g];
-        __syncwarp();
+        if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             mma_ts(tm + 256 + g * 128, tm + g * 128 + x * 8, vd + x * (2048 >> 4), kPv, add || x > 0);
     };
+    auto commit = [&](uint64_t* bar) {
+        if (ok) mma_commit(bar);
+    };
     // The value rows behind the item's last position are zeroed: their weights are zero, and 0 * NaN is NaN.
     auto clear_tail = [&](uint32_t st, int from) {
-        if (L::k8 || from >= kTileRows) return;
+        if (L::k8 || from >= kTileRows || !ok) return;
         uint8_t* v = smem + L::kKv + st * kStageBytes;
         for (int x = from * 8 + lane; x < kTileRows * 8; x += 32) {
             reinterpret_cast<uint4*>(v)[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -489,16 +499,16 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
 
     while (const Segment* s = stretches.next()) {
         const int count = uniform(s->j1 - s->j0), end = uniform(s->end - s->j0 * kTileRows), two = uniform(s->two);
-        pipe_wait(&c.q_full[0], q_count[0] & 1, &c.dead, a.status);
+        ok = pipe_wait(&c.q_full[0], q_count[0] & 1, &c.dead, a.status);
         ++q_count[0];
         if (two) {
-            pipe_wait(&c.q_full[1], q_count[1] & 1, &c.dead, a.status);
+            ok = ok && pipe_wait(&c.q_full[1], q_count[1] & 1, &c.dead, a.status);
             ++q_count[1];
             uint32_t k = wait_stage();
             qk(0, 0, k);
             qk(1, 1, k);
-            mma_commit(&c.kv_empty[k]);
-            for (int t = 0; t < count; ++t) {
+            commit(&c.kv_empty[k]);
+            for (int t = 0; t < count && ok; ++t) {
                 const uint32_t v = wait_stage();
                 const bool more = t + 1 < count;
                 clear_tail(v, end - t * kTileRows);
@@ -506,36 +516,37 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     pv(g, v, t > 0);
-                    if (g == 1) mma_commit(&c.kv_empty[v]);
+                    if (g == 1) commit(&c.kv_empty[v]);
                     if (more) qk(g, g, k);
-                    else mma_commit(&c.o_full[g]);
+                    else commit(&c.o_full[g]);
                 }
-                if (more) mma_commit(&c.kv_empty[k]);
+                if (more) commit(&c.kv_empty[k]);
             }
-            mma_commit(&c.q_empty[0]);
-            mma_commit(&c.q_empty[1]);
+            commit(&c.q_empty[0]);
+            commit(&c.q_empty[1]);
         } else {
             for (int g = 0; g < 2 && g < count; ++g) {
                 const uint32_t k = wait_stage();
                 qk(g, 0, k);
-                mma_commit(&c.kv_empty[k]);
+                commit(&c.kv_empty[k]);
             }
-            for (int t = 0; t < count; ++t) {
+            for (int t = 0; t < count && ok; ++t) {
                 const int g = t & 1;
                 const uint32_t v = wait_stage();
                 clear_tail(v, end - t * kTileRows);
                 pv(g, v, t > 1);
-                mma_commit(&c.kv_empty[v]);
+                commit(&c.kv_empty[v]);
                 if (t + 2 < count) {
                     const uint32_t k = wait_stage();
                     qk(g, 0, k);
-                    mma_commit(&c.kv_empty[k]);
+                    commit(&c.kv_empty[k]);
                 } else {
-                    mma_commit(&c.o_full[g]);
+                    commit(&c.o_full[g]);
                 }
             }
-            mma_commit(&c.q_empty[0]);
+            commit(&c.q_empty[0]);
         }
+        if (!ok) break;
         stretches.done();
     }
     mma_commit(&c.done);   // everything issued has ended before tensor memory is given back
@@ -543,88 +554,93 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
     mbar_wait(&c.done, 0);
 }
 
-// ---- warps 12-15 (8-bit caches): raw tiles to bf16 stages -------------------------------------------------
+// ---- warps 12-19 (8-bit caches): raw tiles to bf16 stages -------------------------------------------------
+// The tile at ring position `at`; its rows from `rows` on become zero.  False: a wait ran out.
+template <int kFmt>
+__device__ __forceinline__ bool expand_tile(const ChunkArgs& a, Control& c, uint8_t* smem, uint32_t at, uint32_t unit, bool v,
+                                            int rows) {
+    using L = Layout<kFmt>;
+    constexpr int kRows = kTileRows / (kExpandThreads / 8);   // rows per thread
+    const int tid = threadIdx.x - Layout<kFmt>::kThreads + kExpandThreads;
+    const uint32_t raw = at % L::kRaw, st = at % L::kStages;
+    if (!pipe_wait(&c.raw_full[raw], (at / L::kRaw) & 1, &c.dead, a.status, &c.kv_empty[st], ((at / L::kStages) & 1) ^ 1))
+        return false;
+    const uint8_t* src = smem + L::kRawOff + raw * kRawBytes;
+    const uint8_t* sc = smem + L::kScaleOff + (unit % L::kScaleSlots) * kScaleTile + (v ? kScaleBytes : 0);
+    uint8_t* dst = smem + L::kKv + st * kStageBytes;
+    const int c16 = tid & 7, h = c16 >> 2, k0 = 2 * (c16 & 3), r0 = tid >> 3;
+    // lanes of the upper half write their second chunk first: eight lanes, eight bank groups
+    auto put = [&](int row, const uint4& o0, const uint4& o1) {
+        uint8_t* line = dst + h * kHalf + row * 128;
+        *reinterpret_cast<uint4*>(line + (((k0 + h) ^ (row & 7)) << 4)) = h ? o1 : o0;
+        *reinterpret_cast<uint4*>(line + (((k0 + 1 - h) ^ (row & 7)) << 4)) = h ? o0 : o1;
+    };
+    uint32_t by[kRows], odd = rows < kTileRows ? 1u : 0u;
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) by[x] = sc[(x * (kTileRows / kRows) + r0) * (2 * kScaleBytes) + (c16 >> 1)];
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) odd |= plain_factor<kFmt>(by[x]) ? 0u : 1u;
+    if (__all_sync(0xffffffffu, odd == 0u)) {   // the loads of all rows, then their arithmetic side by side
+        uint4 e[kRows];
+#pragma unroll
+        for (int x = 0; x < kRows; ++x)
+            e[x] = *reinterpret_cast<const uint4*>(src + (x * (kTileRows / kRows) + r0) * kHeadDim + c16 * 16);
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+            const uint32_t f = factor_plain<kFmt>(by[x]);
+            uint4 o0, o1;
+            expand4<kFmt>(e[x].x, o0.x, o0.y);
+            expand4<kFmt>(e[x].y, o0.z, o0.w);
+            expand4<kFmt>(e[x].z, o1.x, o1.y);
+            expand4<kFmt>(e[x].w, o1.z, o1.w);
+            put(x * (kTileRows / kRows) + r0,
+                make_uint4(mul_bf16x2(o0.x, f), mul_bf16x2(o0.y, f), mul_bf16x2(o0.z, f), mul_bf16x2(o0.w, f)),
+                make_uint4(mul_bf16x2(o1.x, f), mul_bf16x2(o1.y, f), mul_bf16x2(o1.z, f), mul_bf16x2(o1.w, f)));
+        }
+    } else {   // the item's last tile, or a scale at the ends of the range
+#pragma unroll 1
+        for (int x = 0; x < kRows; ++x) {
+            const int row = x * (kTileRows / kRows) + r0;
+            uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;
+            if (row < rows) {
+                const uint4 e = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
+                const Factor f = factor_of<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
+                decode4<kFmt>(e.x, f, o0.x, o0.y);
+                decode4<kFmt>(e.y, f, o0.z, o0.w);
+                decode4<kFmt>(e.z, f, o1.x, o1.y);
+                decode4<kFmt>(e.w, f, o1.z, o1.w);
+            }
+            put(row, o0, o1);
+        }
+    }
+    fence_proxy_async();
+    mbar_arrive(&c.raw_empty[raw]);
+    mbar_arrive(&c.kv_full[st]);
+    return true;
+}
+
 template <int kFmt>
 __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uint8_t* smem) {
-    using L = Layout<kFmt>;
-    const int tid = threadIdx.x & 127;
-    uint32_t ring = 0, unit[2] = {0, 0};
+    uint32_t ring = 0, unit = 0;
     Stretches stretches(c, a.status);
-    auto tile = [&](bool v, int rows) {   // rows from there on become zero
-        const uint32_t raw = ring % L::kRaw, st = ring % L::kStages;
-        pipe_wait(&c.raw_full[raw], (ring / L::kRaw) & 1, &c.dead, a.status);
-        pipe_wait(&c.kv_empty[st], ((ring / L::kStages) & 1) ^ 1, &c.dead, a.status);
-        ++ring;
-        const uint8_t* src = smem + L::kRawOff + raw * kRawBytes;
-        const uint8_t* sc = smem + L::kScaleOff + (unit[v] % 3) * kScaleTile + (v ? kScaleBytes : 0);
-        ++unit[v];
-        uint8_t* dst = smem + L::kKv + st * kStageBytes;
-        const int c16 = tid & 7, h = c16 >> 2, k0 = 2 * (c16 & 3);
-        // lanes of the upper half write their second chunk first: eight lanes, eight bank groups
-        auto put = [&](int row, const uint4& o0, const uint4& o1) {
-            uint8_t* line = dst + h * kHalf + row * 128;
-            *reinterpret_cast<uint4*>(line + (((k0 + h) ^ (row & 7)) << 4)) = h ? o1 : o0;
-            *reinterpret_cast<uint4*>(line + (((k0 + 1 - h) ^ (row & 7)) << 4)) = h ? o0 : o1;
-        };
-        bool plain = rows >= kTileRows;
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-            plain = plain && plain_factor<kFmt>(sc[(x * 16 + (tid >> 3)) * (2 * kScaleBytes) + (c16 >> 1)]);
-        if (__all_sync(0xffffffffu, plain)) {   // the loads of four rows, then their arithmetic side by side
-#pragma unroll 1
-            for (int x0 = 0; x0 < 8; x0 += kExpandRows) {
-                uint4 e[kExpandRows];
-                uint32_t f[kExpandRows];
-#pragma unroll
-                for (int x = 0; x < kExpandRows; ++x) {
-                    const int row = (x0 + x) * 16 + (tid >> 3);
-                    e[x] = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
-                    f[x] = factor_plain<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
-                }
-#pragma unroll
-                for (int x = 0; x < kExpandRows; ++x) {
-                    uint4 o0, o1;
-                    expand4<kFmt>(e[x].x, o0.x, o0.y);
-                    expand4<kFmt>(e[x].y, o0.z, o0.w);
-                    expand4<kFmt>(e[x].z, o1.x, o1.y);
-                    expand4<kFmt>(e[x].w, o1.z, o1.w);
-                    put((x0 + x) * 16 + (tid >> 3),
-                        make_uint4(mul_bf16x2(o0.x, f[x]), mul_bf16x2(o0.y, f[x]), mul_bf16x2(o0.z, f[x]), mul_bf16x2(o0.w, f[x])),
-                        make_uint4(mul_bf16x2(o1.x, f[x]), mul_bf16x2(o1.y, f[x]), mul_bf16x2(o1.z, f[x]), mul_bf16x2(o1.w, f[x])));
-                }
-            }
-        } else {   // the item's last tile, or a scale at the ends of the range
-#pragma unroll 1
-            for (int x = 0; x < 8; ++x) {
-                const int row = x * 16 + (tid >> 3);
-                uint4 o0 = make_uint4(0u, 0u, 0u, 0u), o1 = o0;
-                if (row < rows) {
-                    const uint4 e = *reinterpret_cast<const uint4*>(src + row * kHeadDim + c16 * 16);
-                    const Factor f = factor_of<kFmt>(sc[row * (2 * kScaleBytes) + (c16 >> 1)]);
-                    decode4<kFmt>(e.x, f, o0.x, o0.y);
-                    decode4<kFmt>(e.y, f, o0.z, o0.w);
-                    decode4<kFmt>(e.z, f, o1.x, o1.y);
-                    decode4<kFmt>(e.w, f, o1.z, o1.w);
-                }
-                put(row, o0, o1);
-            }
-        }
-        fence_proxy_async();
-        mbar_arrive(&c.kv_full[st]);
-        mbar_arrive(&c.raw_empty[raw]);
-    };
     while (const Segment* s = stretches.next()) {
         const int count = s->j1 - s->j0, ahead = s->two ? 1 : 2, end = s->end - s->j0 * kTileRows;
-        for (int k = 0; k < 2 * count; ++k) {   // (one loop body: the code of two would crowd the instruction cache)
+        for (int k = 0; k < 2 * count; ++k) {   // (one call: the code of two would crowd the instruction cache)
             int t;
             const bool v = copy_order(k, count, ahead, t);
-            tile(v, end - t * kTileRows);
+            if (!expand_tile<kFmt>(a, c, smem, ring + k, unit + t, v, end - t * kTileRows)) return;
         }
+        ring += 2 * count;
+        unit += count;
         stretches.done();
     }
 }
 
 // ---- warps 0-7: softmax and output --------------------------------------------------------------------------
+// kLook: blocks of 32 scores that are loaded together, and one such step ahead.  Two are faster (4096 tokens over
+// 65536 positions in bf16: 3.64 ms against 3.90), one fits the registers that the 8-bit caches' other warps leave.
+// kFma: of eight pairs of weights, those computed on the FMA pipe (with 8-bit caches it has other work too).
+template <int kLook, int kFma>
 __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
     const int cta = blockIdx.x;
     const int g = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
@@ -646,9 +662,8 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
         float m = -INFINITY, l = 0.f;
         bool begun = false;
         for (int t = s.two ? 0 : g; t < count; t += step) {
-            bool ok = pipe_wait(&c.s_full[g], s_count & 1, &c.dead, a.status);
+            if (!pipe_wait(&c.s_full[g], s_count & 1, &c.dead, a.status)) return;
             ++s_count;
-            if (!__all_sync(0xffffffffu, ok)) continue;
             if (!rows_here) {
                 mbar_arrive(&c.p_full[g]);
                 continue;
@@ -693,31 +708,30 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
                 const uint64_t sc2 = pair_of(scale, scale), sh2 = pair_of(shift, shift);
                 const float scu = scale / 128.f, shu = (shift + 112.f) / 128.f;
                 uint64_t sum[2] = {0ull, 0ull};
-                tmem_ld32(sc, r[0]);
-                tmem_ld32(sc + 32, r[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {   // the second half arrives while the first one is worked on
+                for (int x = 0; x < kLook; ++x) tmem_ld32(sc + x * 32, r[x]);
+#pragma unroll
+                for (int h = 0; h < 4; h += kLook) {   // the next columns arrive while these are worked on
                     tmem_wait_ld();
-                    tmem_loaded(r[2 * h]);
-                    tmem_loaded(r[2 * h + 1]);
-                    if (h == 0) {
-                        tmem_ld32(sc + 64, r[2]);
-                        tmem_ld32(sc + 96, r[3]);
+#pragma unroll
+                    for (int x = h; x < h + kLook; ++x) {
+                        tmem_loaded(r[x]);
+                        if (x + kLook < 4) tmem_ld32(sc + (x + kLook) * 32, r[x + kLook]);
                     }
                     if (border) {
 #pragma unroll
-                        for (int x = 2 * h; x < 2 * h + 2; ++x)
+                        for (int x = h; x < h + kLook; ++x)
 #pragma unroll
                             for (int y = 0; y < 32; ++y)
                                 if (x * 32 + y > last) r[x][y] = 0xff800000u;
                     }
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) {   // pair y takes the place of values that were used before
-                        const uint32_t(&src)[32] = r[2 * h + (y >> 4)];
+                    for (int y = 0; y < 16 * kLook; ++y) {   // pair y takes the place of values that were used before
+                        const uint32_t(&src)[32] = r[h + (y >> 4)];
                         const int z = (y & 15) * 2;
                         float lo = __uint_as_float(src[z]), hi = __uint_as_float(src[z + 1]);
                         uint64_t e;
-                        if ((y & 7) < kFmaOf8) {
+                        if ((y & 7) < kFma) {
                             e = ex2_fma2(pair_of(fma_sat(lo, scu, shu), fma_sat(hi, scu, shu)));
                             split_pair(e, lo, hi);
                         } else {
@@ -727,7 +741,7 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
                             e = pair_of(lo, hi);
                         }
                         sum[y & 1] = add2(sum[y & 1], e);
-                        r[2 * h][y] = pack_bf16x2(lo, hi);
+                        r[h][y] = pack_bf16x2(lo, hi);
                     }
                 }
                 float s0, s1;
@@ -738,8 +752,11 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
             }
             l += add;
             begun = true;
-            tmem_st32(sc, r[0]);
-            tmem_st32(sc + 32, r[2]);
+#pragma unroll
+            for (int h = 0; h < 4; h += kLook) {
+                if (kLook == 1) tmem_st16(sc + h * 16, r[h]);
+                else tmem_st32(sc + h * 16, r[h]);
+            }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&c.p_full[g]);
@@ -747,10 +764,9 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
         // the stretch's output: final rows, or a part for the merge
         const bool mine = s.two || g < count;
         if (mine) {
-            pipe_wait(&c.o_full[g], o_count & 1, &c.dead, a.status);
+            if (!pipe_wait(&c.o_full[g], o_count & 1, &c.dead, a.status)) return;
             ++o_count;
         }
-        __syncwarp();
         tc_fence_after();
         const bool whole = s.j0 == 0 && s.j1 == s.tiles;
         const int slot = 2 * cta + (s.j0 > 0 ? 0 : 1);
@@ -761,8 +777,7 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
             c.post[g * kTileRows + row] = make_float2(m, l);
             tc_fence_before();
             mbar_arrive(&c.join[0]);
-            pipe_wait(&c.join[0], joins & 1, &c.dead, a.status);
-            __syncwarp();
+            if (!pipe_wait(&c.join[0], joins & 1, &c.dead, a.status)) return;
             tc_fence_after();
             const float2 p0 = c.post[row], p1 = c.post[kTileRows + row];
             m = fmaxf(p0.x, p1.x);
@@ -816,9 +831,8 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
         tc_fence_before();
         if (!s.two) {   // both sides have read before either goes on
             mbar_arrive(&c.join[1]);
-            pipe_wait(&c.join[1], joins & 1, &c.dead, a.status);
+            if (!pipe_wait(&c.join[1], joins & 1, &c.dead, a.status)) return;
             ++joins;
-            __syncwarp();
         }
         if (threadIdx.x == 0 && s.last >= 0)
             reinterpret_cast<TailRecord*>(a.tail)[cta] = TailRecord{1, s.rows, s.tokens, s.kvh, s.last, {}};
@@ -844,16 +858,16 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
             mbar_init(&c.join[x], 256);
         }
         for (int x = 0; x < L::kStages; ++x) {
-            mbar_init(&c.kv_full[x], L::k8 ? 128 : 1);
+            mbar_init(&c.kv_full[x], L::k8 ? kExpandThreads : 1);
             mbar_init(&c.kv_empty[x], 1);
         }
         for (int x = 0; x < L::kRaw; ++x) {
             mbar_init(&c.raw_full[x], 1);
-            mbar_init(&c.raw_empty[x], 128);
+            mbar_init(&c.raw_empty[x], kExpandThreads);
         }
         for (int x = 0; x < kSegments; ++x) {
             mbar_init(&c.seg_full[x], 1);
-            mbar_init(&c.seg_empty[x], L::k8 ? 14 : 10);   // the warps that read them
+            mbar_init(&c.seg_empty[x], L::k8 ? 18 : 10);   // the warps that read them
         }
         mbar_init(&c.done, 1);
         c.dead = 0;
@@ -867,14 +881,14 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     long long u0, u1, total;
     plan(a, c, u0, u1, total);
     if (warp < 8) {
-        regs_up<L::k8 ? 200 : 216>();
-        softmax_warps(a, c);
+        regs_up<L::k8 ? 136 : 216>();
+        softmax_warps<L::k8 ? 1 : 2, L::k8 ? 1 : 2>(a, c);
     } else if (warp < 12) {
-        regs_down<L::k8 ? 48 : 72>();
+        regs_down<L::k8 ? 64 : 72>();
         if (warp == 8 || warp == 10) copy_warps<kFmt>(a, c, smem, warp == 10, Walk(a, c, u0, u1, total), &qm, warp == 10 ? &vm : &km);
         if (warp == 9) mma_warp<kFmt>(a, c, smem);
     } else if (L::k8) {
-        regs_down<64>();
+        regs_down<72>();
         expand_warps<kFmt>(a, c, smem);
     }
     tc_fence_before();

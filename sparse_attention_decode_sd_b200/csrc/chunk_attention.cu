@@ -67,6 +67,10 @@ struct Layout {
     static constexpr int kThreads = k8 ? 640 : 384;
 };
 
+struct Request {
+    int rs, n, base;   // first row, new rows, positions before them
+};
+
 constexpr int kSegments = 4;   // stretches that the copies may run ahead
 
 // One stretch of consecutive units of one item.
@@ -93,6 +97,7 @@ struct Control {
     uint32_t tmem;
     int dead;                // a wait ran out: nothing more is issued
     int b, kvh, pair, unit;  // where this CTA's share starts
+    Request start;           // the request of b
     long long scan[20];
     float2 post[2 * kTileRows];   // maximum and sum of the two sides of a one-tile item
 };
@@ -130,9 +135,6 @@ __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, int* d
 }
 
 // ---- the batch as units --------------------------------------------------------------------------------
-struct Request {
-    int rs, n, base;   // first row, new rows, positions before them
-};
 __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
     Request r;
     r.rs = a.row_start[b];
@@ -166,6 +168,21 @@ __device__ __forceinline__ long long tiles_before(const Request& r, int i, int i
 // CTAs that get units: each of them at least one, so that the parts of a cut item lie in neighbouring CTAs.
 __device__ __forceinline__ long long shares(long long total) { return min(total, (long long)gridDim.x); }
 
+// The first unit of CTA c's share.  (A 64-bit division costs hundreds of cycles, and the start of a short call counts.)
+__device__ __forceinline__ long long share_begin(long long total, uint32_t c) {
+    const uint32_t parts = (uint32_t)shares(total);
+    if (c >= parts) return total;
+    if (total < (1ll << 24)) return (uint32_t)total * c / parts;   // (c is below 2^8)
+    return total * c / parts;
+}
+
+// The CTA that has unit end - 1.
+__device__ __forceinline__ int last_share(long long total, long long end) {
+    const uint32_t parts = (uint32_t)shares(total);
+    if (total < (1ll << 24)) return (int)(((uint32_t)end * parts - 1) / (uint32_t)total);
+    return (int)((end * parts - 1) / total);
+}
+
 // A CTA's share as stretches, for the copy warp.
 struct Walk {
     const ChunkArgs& a;
@@ -175,7 +192,7 @@ struct Walk {
     __device__ Walk(const ChunkArgs& args, const Control& c, long long begin, long long end, long long all)
         : a(args), w(2 * args.tpt), b(c.b), kvh(c.kvh), i(c.pair), j(c.unit), left(end - begin), u1(end), total(all) {
         if (left > 0) {
-            r = request(a, b);
+            r = c.start;
             items = (r.n + w - 1) / w;
         }
     }
@@ -194,7 +211,7 @@ struct Walk {
         left -= s.j1 - s.j0;
         s.last = -1;
         if (left == 0 && s.j0 == 0 && s.j1 < s.tiles)
-            s.last = (int)(((u1 - s.j1 + s.tiles) * shares(total) - 1) / total);
+            s.last = last_share(total, u1 - s.j1 + s.tiles);
         j = s.j1;
         if (left > 0) {   // the stretch ended with its item
             j = 0;
@@ -218,8 +235,9 @@ struct TailRecord {
     int valid, rows, tokens, kvh, last, pad[3];
 };
 
-__device__ __forceinline__ float* slot_out(const ChunkArgs& a, int slot) {
-    return a.part + (long)slot * (2 * kTileRows) * kHeadDim;
+// A slot: [32 chunks of four dimensions][256 rows], so that the threads that hold a row each write whole lines.
+__device__ __forceinline__ float4* slot_out(const ChunkArgs& a, int slot, int chunk) {
+    return reinterpret_cast<float4*>(a.part) + ((long)slot * (kHeadDim / 4) + chunk) * (2 * kTileRows);
 }
 __device__ __forceinline__ float2* slot_ml(const ChunkArgs& a, int slot) { return a.ml + (long)slot * (2 * kTileRows); }
 
@@ -230,7 +248,8 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
     const int per = (a.B + blockDim.x - 1) / blockDim.x, w = 2 * a.tpt;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     bool bad = false;
-    long long mine = 0;
+    long long mine = 0, head = 0;   // (head, last: of the thread's last request, most often its only one)
+    Request last = {0, 0, 0};
     for (int b = b0; b < b1; ++b) {
         const int lo = a.row_start[b], hi = a.row_start[b + 1];
         bad = bad || lo < 0 || hi < lo || hi > a.total_rows;
@@ -240,9 +259,10 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
             continue;
         }
         if (bad || hi == lo) continue;
-        const Request r = {lo, hi - lo, N - (hi - lo)};
-        const int items = (r.n + w - 1) / w;
-        mine += a.Hkv * tiles_before(r, items, items, w);
+        last = Request{lo, hi - lo, N - (hi - lo)};
+        const int items = (last.n + w - 1) / w;
+        head = tiles_before(last, items, items, w);
+        mine += a.Hkv * head;
     }
     if (__syncthreads_or(bad ? 1 : 0)) {
         if (tid == 0 && blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
@@ -263,22 +283,22 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
         if (x < warp) before += c.scan[x];
         total += c.scan[x];
     }
-    const long long parts = shares(total);
-    u0 = min((long long)blockIdx.x, parts) * total / max(parts, 1ll);
-    u1 = min((long long)blockIdx.x + 1, parts) * total / max(parts, 1ll);
+    u0 = share_begin(total, blockIdx.x);
+    u1 = share_begin(total, blockIdx.x + 1);
     if (u1 > u0 && before <= u0 && u0 < before + mine) {   // the share starts in this thread's requests
         long long at = u0 - before;
         for (int b = b0; b < b1; ++b) {
-            const Request r = request(a, b);
+            const Request r = per == 1 ? last : request(a, b);
             if (r.n == 0) continue;
             const int items = (r.n + w - 1) / w;
-            const long long head = tiles_before(r, items, items, w);
+            if (per > 1) head = tiles_before(r, items, items, w);
             if (at >= head * a.Hkv) {
                 at -= head * a.Hkv;
                 continue;
             }
             c.b = b;
-            c.kvh = (int)(at / head);
+            c.start = r;
+            c.kvh = at < (1ll << 31) && head < (1ll << 31) ? (int)((uint32_t)at / (uint32_t)head) : (int)(at / head);
             at -= c.kvh * head;
             int lo = 0, hi = items - 1;   // the last item with tiles_before <= at
             while (lo < hi) {
@@ -822,9 +842,11 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
                     dst[y] = make_uint4(v[0], v[1], v[2], v[3]);
                 }
             } else if (valid) {
-                uint4* dst = reinterpret_cast<uint4*>(slot_out(a, slot) + (long)(tile * kTileRows + row) * kHeadDim) + x * 8;
 #pragma unroll
-                for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[y * 4], o[y * 4 + 1], o[y * 4 + 2], o[y * 4 + 3]);
+                for (int y = 0; y < 8; ++y)
+                    slot_out(a, slot, x * 8 + y)[tile * kTileRows + row] =
+                        make_float4(__uint_as_float(o[y * 4]), __uint_as_float(o[y * 4 + 1]), __uint_as_float(o[y * 4 + 2]),
+                                    __uint_as_float(o[y * 4 + 3]));
             }
         }
         if (valid && !whole && (s.two || g == 0)) slot_ml(a, slot)[tile * kTileRows + row] = make_float2(m * scale, l);
@@ -897,35 +919,55 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     if (warp == 9) tmem_dealloc(c.tmem, 512);
 }
 
-// Joins the parts of the items that a CTA's border cut: block (c, y) those of the item that began in CTA c,
-// one warp per row, four output dimensions per lane.
-constexpr int kMergeY = 8, kMergeWarpsChunk = 8;
-__global__ void __launch_bounds__(kMergeWarpsChunk * 32) merge_chunks_kernel(const __grid_constant__ ChunkArgs a) {
+// Joins the parts of the items that CTA borders cut.  A warp takes 32 rows (a lane each) and four dimensions, so that its
+// reads of the parts are whole lines; every block reads all tail records at once and its warps take their work in
+// turn.  A short call then waits for few loads in a row.
+constexpr int kMergeThreads = 256;
+static_assert(kMergeThreads >= kChunkCtas, "one thread per tail record");
+__global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
+    __shared__ TailRecord recs[kChunkCtas];
+    __shared__ int before[kChunkCtas + 1], scratch[40];
     pdl_enter();
-    const TailRecord rec = reinterpret_cast<const TailRecord*>(a.tail)[blockIdx.x];
-    if (!rec.valid) return;
-    const int lane = threadIdx.x & 31, rows = a.tpt * a.G;
-    for (int k = blockIdx.y + kMergeY * (threadIdx.x >> 5); k < rec.tokens * a.G; k += kMergeY * kMergeWarpsChunk) {
+    const int tid = threadIdx.x, lane = tid & 31, rows = a.tpt * a.G;
+    int mine = 0, total;   // blocks of 32 rows
+    if (tid < ctas) {
+        recs[tid] = reinterpret_cast<const TailRecord*>(a.tail)[tid];
+        if (recs[tid].valid) mine = (recs[tid].tokens * a.G + 31) / 32;
+    }
+    const int at = block_exclusive_scan(mine, scratch, &total);
+    if (tid < ctas) before[tid] = at;
+    if (tid == 0) before[ctas] = total;
+    __syncthreads();
+    total *= kHeadDim / 4;
+    for (int w = blockIdx.x + gridDim.x * (tid >> 5); w < total; w += gridDim.x * (kMergeThreads / 32)) {
+        const int block = w / (kHeadDim / 4), chunk = w - block * (kHeadDim / 4);
+        int c = 0, hi = ctas - 1;   // the last CTA with before <= block
+        while (c < hi) {
+            const int mid = (c + hi + 1) >> 1;
+            if (before[mid] <= block) c = mid;
+            else hi = mid - 1;
+        }
+        const TailRecord& rec = recs[c];
+        const int k = (block - before[c]) * 32 + lane;
+        if (k >= rec.tokens * a.G) continue;
         const int tile = k / rows, r = k - tile * rows, row = tile * kTileRows + r;
-        const int first = 2 * blockIdx.x + 1;   // slots: this CTA's second, then the first of each later CTA
-        float m = slot_ml(a, first)[row].x;
-        for (int x = blockIdx.x + 1; x <= rec.last; ++x) m = fmaxf(m, slot_ml(a, 2 * x)[row].x);
+        float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int x = blockIdx.x; x <= rec.last; ++x) {
-            const int slot = x == (int)blockIdx.x ? first : 2 * x;
+#pragma unroll 8
+        for (int x = c; x <= rec.last; ++x) {   // slots: this CTA's second, then the first of each later CTA
+            const int slot = 2 * x + (x == c ? 1 : 0);
             const float2 ml = slot_ml(a, slot)[row];
-            const float4 v = reinterpret_cast<const float4*>(slot_out(a, slot) + (long)row * kHeadDim)[lane];
-            const float f = ex2(ml.x - m);
-            l = fmaf(ml.y, f, l);
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
+            const float4 v = slot_out(a, slot, chunk)[row];
+            const float top = fmaxf(m, ml.x), f = m == -INFINITY ? 0.f : ex2(m - top), g = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+            m = top;
+            l = fmaf(l, f, ml.y * g);
+            o.x = fmaf(o.x, f, v.x * g);
+            o.y = fmaf(o.y, f, v.y * g);
+            o.z = fmaf(o.z, f, v.z * g);
+            o.w = fmaf(o.w, f, v.w * g);
         }
         const float inv = 1.f / l;
-        const long dst = ((long)(rec.rows + tile * a.tpt + r / a.G) * a.Hq + rec.kvh * a.G + r % a.G) * 32 + lane;
+        const long dst = ((long)(rec.rows + tile * a.tpt + r / a.G) * a.Hq + rec.kvh * a.G + r % a.G) * 32 + chunk;
         reinterpret_cast<uint2*>(a.out)[dst] =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
@@ -983,7 +1025,7 @@ cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
     e = launch_pdl(chunk_attention_kernel<kFmt>, dim3(ctas), dim3(Layout<kFmt>::kThreads), chunk_smem<kFmt>(), stream, a, qm,
                    km, vm);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(merge_chunks_kernel, dim3(ctas, kMergeY), dim3(kMergeWarpsChunk * 32), 0, stream, a);
+    e = launch_pdl(merge_chunks_kernel, dim3(2 * ctas), dim3(kMergeThreads), 0, stream, a, ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

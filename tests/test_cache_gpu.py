@@ -224,3 +224,49 @@ def test_many_requests():
     assert int(d.status.item()) == 0
     el, by = ch.quantise(k, "mxint8")
     assert torch.equal(ko.double().cpu(), ch.values(el, by, "mxint8"))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_no_rows_at_all(fmt):
+    """Requests without new rows, empty contexts: nothing is touched."""
+    w = ch.Batch([0, 0, 0], [0, 40, 16], 2, 2, fmt, pad=5)
+    d = w.gpu()
+    before = [x.clone() for x in (d.K.view(torch.uint8), d.V.view(torch.uint8))]
+    k = torch.ones((w.T, 2, 128), dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(k, 7.0)
+    first = torch.tensor([0, 40, 3], dtype=torch.int32, device=DEV)
+    sdb.sd_cache_write(d.shape, d.cache, d.page_table, d.lens, d.row_start, k, k, None, d.status)
+    sdb.sd_cache_read(d.shape, d.cache, d.page_table, d.lens, first, d.row_start, out, None, d.status)
+    att = d.chunk()
+    assert int(d.status.item()) == 0
+    assert (out == 7.0).all() and (att == 7.0).all()
+    for x, y in zip(before, (d.K.view(torch.uint8), d.V.view(torch.uint8))):
+        assert torch.equal(x, y)
+
+
+def test_write_and_read_captured():
+    """One graph of write and read, replayed with other rows and other lengths in the same buffers."""
+    w = ch.Batch([2, 30], [60, 40], 2, 2, "mxint8", seed=4)
+    d = w.gpu()
+    k, v, ko, vo = (torch.zeros((w.T, 2, 128), dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    first = torch.zeros(2, dtype=torch.int32, device=DEV)
+
+    def step():
+        sdb.sd_cache_write(d.shape, d.cache, d.page_table, d.lens, d.row_start, k, v, None, d.status)
+        sdb.sd_cache_read(d.shape, d.cache, d.page_table, d.lens, first, d.row_start, ko, vo, d.status)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed, lens in ((1, [62, 70]), (2, [50, 33])):
+        src = [torch.randn((w.T, 2, 128), generator=torch.Generator().manual_seed(seed + 9 * i)).bfloat16() for i in range(2)]
+        k.copy_(src[0])
+        v.copy_(src[1])
+        d.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        first.copy_(torch.tensor([n - m for n, m in zip(lens, w.n)], dtype=torch.int32))
+        g.replay()
+        assert int(d.status.item()) == 0
+        for s, o in zip(src, (ko, vo)):
+            assert torch.equal(o.double().cpu(), ch.values(*ch.quantise(s, "mxint8"), "mxint8"))

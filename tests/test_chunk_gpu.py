@@ -214,3 +214,56 @@ def test_prompt_in_chunks_equals_the_prompt(fmt):
         at += m
     assert at == n and int(d.status.item()) == 0
     ch.check_attention(out, w, ref)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "mxint8"])
+def test_scores_far_above_the_first_tile(fmt):
+    """Scores that jump by hundreds of powers of two between tiles, up and down, and stay equal: the reference of a row
+    is taken anew where they rise, and small weights vanish where they fall.  (q and K are exact powers of two here, so
+    scores are exact and the bound of the weights' rounding alone holds.)"""
+    w = ch.Batch([2, 150], [600, 500], 8, 2, fmt, seed=14)
+    w.q = torch.ones_like(w.q)
+    for b in range(2):
+        for p in range(w.total[b]):
+            step = [0.0, 4.0, -2.0, 16.0, 16.0, 64.0, 1.0][(p // 100) % 7]
+            w.src[0][int(w.page_table[b, p // 16]), p % 16] = step
+    w.encode()
+    d = w.gpu()
+    ch.check_attention(d.chunk(), w)
+    assert int(d.status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxint8"])
+def test_many_requests_and_idle_ones(fmt):
+    """More requests than the threads that plan the shares, most of them without rows."""
+    B = 1500
+    n = [1 if b % 7 == 3 else 0 for b in range(B)]
+    w = ch.Batch(n, [b % 40 for b in range(B)], 4, 2, fmt, seed=15)
+    d = w.gpu()
+    ch.check_attention(d.chunk(), w)
+    assert int(d.status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_workspace_shared_in_one_stream(fmt):
+    """Calls of different batches one after the other through one workspace, and two graphs that hold it."""
+    ws_ = [ch.Batch([3, 70], [900, 100], 8, 2, fmt, seed=16), ch.Batch([1] * 9, [100 * i for i in range(9)], 16, 4, fmt, seed=17)]
+    ds = [w.gpu() for w in ws_]
+    work = sdb.workspace_for(ds[0].shape, sdb.SD_OP_CHUNK, DEV)
+    refs = [w.attention() for w in ws_]
+    outs = [torch.full((w.T, w.Hq, 128), 7.0, dtype=torch.bfloat16, device=DEV) for w in ws_]
+    graphs = []
+    for d, o in zip(ds, outs):
+        d.chunk(out=o, ws=work)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.chunk(out=o, ws=work)
+        graphs.append(g)
+    for _ in range(2):
+        for g, o in zip(graphs, outs):
+            o.fill_(7.0)
+            g.replay()
+        for o, w, r in zip(outs, ws_, refs):
+            ch.check_attention(o, w, r)
+    assert all(int(d.status.item()) == 0 for d in ds)

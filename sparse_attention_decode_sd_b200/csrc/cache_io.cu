@@ -12,7 +12,7 @@
 // B200: 4 x 16384 rows x 8 heads from bf16 to MXFP8 with boxes 94 us (424 MB: 4.5 TB/s; one row per unit and a walk over the
 // page for its box took 383 us, two fp32 factors per value instead of one bf16 product 117 us); 131072 rows x 8 heads
 // of MXFP8 to bf16 139 us (814 MB: 5.8 TB/s); a decode step of 32 requests 8 us.
-#include "cache_format.cuh"
+#include "cache_half.cuh"
 #include "kernels.h"
 
 namespace sd {
@@ -36,11 +36,6 @@ __device__ __forceinline__ int request_of(const int* prefix, int B, int run) {
     return lo;
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 // The largest magnitude of eight bf16, as bf16 bits (infinities and NaN are the largest).
 __device__ __forceinline__ uint32_t abs_max(const uint4& v) {
     const uint32_t m = max_u16x2(max_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), max_u16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));

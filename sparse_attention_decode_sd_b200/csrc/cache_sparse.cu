@@ -25,9 +25,7 @@
 // What bounds it: random 128-byte rows.  At 4 x 64 heads x 2621 rows of N = 131072 (168 MB with each row of a group
 // read once) the gathers alone take 52 us for K and V, 4 us more for the scales' 32-byte sectors, and 27-40 us when
 // the same number of rows is read in order; the whole call takes 64 us.
-#include <cuda_fp16.h>
-
-#include "cache_format.cuh"
+#include "cache_half.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
 
@@ -69,34 +67,6 @@ __device__ __forceinline__ float exponent_of(uint32_t byte) {
     return byte == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)byte - (kFmt == kFmtFp8 ? 127 : 133));
 }
 
-// The elements in the low (hi = 0) or high two bytes of w as a half-precision pair.  int8 as 1024 + (x + 128) less 1152.
-template <int kFmt, int hi>
-__device__ __forceinline__ uint32_t half_pair(uint32_t w) {
-    uint32_t r;
-    if (kFmt == kFmtFp8) {
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(hi ? w >> 16 : w)));
-    } else {
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w ^ 0x80808080u, 0x64646464u, hi ? 0x4342 : 0x4140)), "r"(0x64806480u));
-    }
-    return r;
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same with zeros in the lower eight rows of A: only the upper rows of the result are kept.
-__device__ __forceinline__ void mma_f16_upper(float (&c)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-    [[maybe_unused]] float x, y;
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%8,%5,%8}, {%6,%7}, {%0,%1,%9,%9};\n"
-        : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
-        : "r"(a0), "r"(a2), "r"(b0), "r"(b1), "r"(0u), "f"(0.f));
-}
-
 __device__ __forceinline__ float* part_out(const CacheSparseArgs& a, long slot) { return a.part + slot * kHeadDim; }
 
 template <int kFmt>
@@ -134,10 +104,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
         for (int x = 0; x < 8; ++x) big = fmaxf(big, fabsf(q[x]));
 #pragma unroll
         for (int x = 16; x; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-        // the power of two at or below the largest value (of the smallest normal number where that is less)
-        const uint32_t top_bits = max(__float_as_uint(big) & 0x7f800000u, 0x00800000u);
-        const float down = __uint_as_float(0x7f000000u - min(top_bits, 0x7e800000u));
-        const float up = __uint_as_float(min(top_bits, 0x7e800000u)) * a.scale_log2;
+        float down, up;
+        power_of_two(big, down, up);
+        up *= a.scale_log2;
         uint32_t qb[2][2];   // [half of the block][k, k + 8]
 #pragma unroll
         for (int x = 0; x < 4; ++x) {

@@ -33,13 +33,11 @@
 // Items of one tile (few tokens: decode, short chunks) split their units between the two warpgroups, even and odd,
 // each with a maximum, sum and output of its own, joined at the end: the two sides stay busy in turn all the same.
 #include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
 
 #include "cache_format.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace sd {
 
@@ -973,52 +971,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __gri
     }
 }
 
-struct Encoder {
-    std::mutex mu;
-    PFN_cuTensorMapEncodeTiled fn = nullptr;
-};
-Encoder g_encoder;
-
-cudaError_t encoder(PFN_cuTensorMapEncodeTiled* out) {
-    std::lock_guard<std::mutex> lock(g_encoder.mu);
-    if (g_encoder.fn == nullptr) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return e;
-        if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
-        g_encoder.fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(fn);
-    }
-    *out = g_encoder.fn;
-    return cudaSuccess;
-}
-
-// [rows][heads][128] with a box of {x values, y heads, z rows}
-bool encode3(PFN_cuTensorMapEncodeTiled fn, CUtensorMap* m, const void* base, bool bytes, long heads, long rows, int x,
-             int y, int z) {
-    const cuuint64_t esz = bytes ? 1 : 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)rows};
-    const cuuint64_t strides[2] = {kHeadDim * esz, kHeadDim * esz * (cuuint64_t)heads};
-    const cuuint32_t box[3] = {(cuuint32_t)x, (cuuint32_t)y, (cuuint32_t)z};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int kFmt>
 cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
-    PFN_cuTensorMapEncodeTiled fn;
-    cudaError_t e = encoder(&fn);
-    if (e != cudaSuccess) return e;
     constexpr bool k8 = Layout<kFmt>::k8;
     CUtensorMap qm, km, vm;
     const long rows = (long)a.num_pages * kPageSize;
-    if (!encode3(fn, &qm, a.q, false, a.Hq, a.total_rows, 64, a.G, a.tpt) ||
-        !encode3(fn, &km, a.K, k8, a.Hkv, rows, k8 ? kHeadDim : 64, 1, kPageSize) ||
-        !encode3(fn, &vm, a.V, k8, a.Hkv, rows, k8 ? kHeadDim : 64, 1, kPageSize))
-        return cudaErrorInvalidValue;
+    cudaError_t e = encode_rows_map(&qm, a.q, false, a.Hq, a.total_rows, 64, a.G, a.tpt, true);
+    if (e == cudaSuccess) e = encode_rows_map(&km, a.K, k8, a.Hkv, rows, k8 ? kHeadDim : 64, 1, kPageSize, !k8);
+    if (e == cudaSuccess) e = encode_rows_map(&vm, a.V, k8, a.Hkv, rows, k8 ? kHeadDim : 64, 1, kPageSize, !k8);
+    if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(chunk_attention_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize, chunk_smem<kFmt>());
     if (e != cudaSuccess) return e;
     const int ctas = a.sms < kChunkCtas ? a.sms : kChunkCtas;
@@ -1033,14 +994,20 @@ cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
 
 ChunkLayout chunk_layout() {
     ChunkLayout L;
+    // two slots per CTA: of 256 rows here, of 8 rows in cache_decode.cu
+    const size_t slots = (size_t)2 * kChunkCtas * 2 * kTileRows, few = (size_t)2 * kDecodeShares * 8;
+    const size_t rows = slots > few ? slots : few;
     L.part = 0;
-    L.ml = (size_t)2 * kChunkCtas * 2 * kTileRows * kHeadDim * sizeof(float);
-    L.tail = L.ml + (size_t)2 * kChunkCtas * 2 * kTileRows * sizeof(float2);
-    L.total = (L.tail + kChunkCtas * sizeof(TailRecord) + 255) / 256 * 256;
+    L.ml = rows * kHeadDim * sizeof(float);
+    L.tail = L.ml + rows * sizeof(float2);
+    L.total = L.tail + (size_t)kDecodeShares * sizeof(TailRecord);
     return L;
 }
 
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream) {
+    // 8-bit caches and at most eight rows to a KV head and request on the average: 32 single tokens over 8K-164K positions
+    // take FEWROWS; either way every batch gives its result.
+    if (format != kFmtBf16 && a.G <= 8 && (long)a.total_rows * a.G <= 8l * a.B) return launch_cache_decode(a, format, stream);
     return format == kFmtBf16 ? launch_format<kFmtBf16>(a, stream)
            : format == kFmtFp8 ? launch_format<kFmtFp8>(a, stream) : launch_format<kFmtInt8>(a, stream);
 }

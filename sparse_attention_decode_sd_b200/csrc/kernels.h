@@ -200,6 +200,9 @@ struct ChunkLayout {
 };
 ChunkLayout chunk_layout();
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream);
+// The same for few rows per KV head over an 8-bit cache (cache_decode.cu).
+constexpr int kDecodeShares = 2048;   // warps of one wave at most
+cudaError_t launch_cache_decode(const ChunkArgs& a, int format, cudaStream_t stream);
 
 // Sparse decode over an 8-bit cache (cache_sparse.cu).
 struct CacheSparseArgs {

@@ -8,11 +8,16 @@
 // half-precision fragments, which hold them exactly (mma.sync m16n8k16, the eight rows in the upper half of A):
 //   scores   A = q (scaled by a power of two to at most 2 per row), B = K; each block of 32 dimensions has its own
 //            accumulator, which takes the block's scale of that position in fp32.
-//   outputs  A = the weights, once for each block x: w_i 2^(e_x(i) - r_x), B = V, so that block x of V needs no scaling;
-//            r_x is the largest scale of the block so far.
-// Weights are exp2(s - m) for a running maximum m that may lag by 2^8; they enter as half precision (11 bits), their
-// sum is fp32.  All steps of the batch are cut evenly over the warps of one wave; items cut by a border leave parts
+//   outputs  A = the weights, once for each block x: p_i 2^(e_x(i)) c_x with p_i = exp2(s_i - m), B = V, so that block x
+//            of V needs no scaling.  m is a running maximum of the scores that may lag by 2^8, and c_x a factor of the
+//            row and block that keeps the largest product so far near 2^6: half precision has few exponents, and where
+//            the largest scale stands beside a small weight it must not push the others out.
+// Weights enter as half precision (11 bits); their sum is fp32.  All steps of the batch are cut evenly over the warps of one wave; items cut by a border leave parts
 // in the workspace, which merge_decode_kernel joins in order.
+//
+// What bounds it: instructions (about 580 per page of 16 positions; the schedulers issue 60% of the time with 12
+// warps per SM, and 16 warps spill registers: 1.51 ms instead of 1.19).  32 single tokens over 8K-164K positions, 32/8
+// heads: 1.19 ms in MXFP8 (5.6 GB, 4.7 TB/s), 1.44 ms in MXINT8, whose elements take one more instruction per pair.
 #include "cache_half.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -26,7 +31,9 @@ constexpr int kRows = 8;                     // rows of an item
 constexpr int kRing = 4;                     // steps in a warp's ring
 constexpr int kCtasPerSm = 12;               // one warp each
 constexpr float kGrow = 8.f;                 // log2 units that the maximum may lag behind
-constexpr int kLift = 6;                     // weights reach up to 2^(8 + kLift), clear of half precision's ends
+constexpr int kLift = 6;                     // log2 of what the largest weight is scaled to
+constexpr float kTop = 16384.f;              // weights from here on (half precision ends at 65504) rescale their row
+constexpr float kMostFactor = 1.2676506e30f; // 2^100: c_x at most
 
 struct Stage {
     uint8_t k[kPageSize][kHeadDim], v[kPageSize][kHeadDim];
@@ -189,8 +196,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y) o[x][y][0] = o[x][y][1] = 0.f;
-        uint32_t ref_even = 0u, ref_odd = 0u;   // largest scale bytes of V so far: blocks 0, 2 and 1, 3 (halves)
-        float unscale[4] = {0.f, 0.f, 0.f, 0.f};   // 2^(kLift - r_x)
+        float c[4] = {1.f, 1.f, 1.f, 1.f};          // (set when the row sees its first position)
 
         // page-table entries: 32 steps at a time, a lane each, the next 32 on their way
         const int32_t* table = a.page_table + (long)b * a.max_pages;
@@ -257,50 +263,65 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
                 if (border && p0 + 2 * kq + (y & 1) + 8 * (y >> 1) > lim) s[y] = -INFINITY;
             }
             const float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-            // V's scales: a block whose largest grows takes a new reference
-            uint32_t even = ref_even, odd = ref_odd;
             if (border) {
 #pragma unroll
                 for (int y = 0; y < 4; ++y)   // (what lies behind the last position does not count)
                     if (p0 + 2 * kq + (y & 1) + 8 * (y >> 1) >= end) sc[y].y = 0u;
             }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                even = max_u16x2(even, sc[y].y & 0x00ff00ffu);
-                odd = max_u16x2(odd, sc[y].y >> 8 & 0x00ff00ffu);
-            }
-            if (__any_sync(0xffffffffu, top - m > kGrow || even != ref_even || odd != ref_odd)) {
+            bool fresh = false;
+            if (__any_sync(0xffffffffu, top - m > kGrow)) {   // (from -infinity: any finite score)
                 float mt = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 mt = fmaxf(m, fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2)));
                 const float f = mt > m ? ex2(m - mt) : 1.f;
+                fresh = m == -INFINITY && mt > m;
                 m = mt;
                 l *= f;
 #pragma unroll
-                for (int i = 1; i < 4; i <<= 1) {
-                    even = max_u16x2(even, __shfl_xor_sync(0xffffffffu, even, i));
-                    odd = max_u16x2(odd, __shfl_xor_sync(0xffffffffu, odd, i));
-                }
+                for (int x = 0; x < 4; ++x) {   // the products' references stay where they are, as far as c reaches
+                    const float now = fminf(c[x] / f, kMostFactor), g = now / c[x] * f;
+                    if (mt > -INFINITY && f != 1.f) {
+                        c[x] = now;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int now = (int)((x & 1 ? odd : even) >> (16 * (x >> 1)) & 255u);
-                    const int was = (int)((x & 1 ? ref_odd : ref_even) >> (16 * (x >> 1)) & 255u);
-                    const float g = f * ex2((float)(was - now));
-                    unscale[x] = __uint_as_float((uint32_t)min(254 + kLift - now, 254) << 23);   // 2^(127 + kLift - now)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        o[x][y][0] *= g;
-                        o[x][y][1] *= g;
+                        for (int y = 0; y < 4; ++y) {
+                            o[x][y][0] *= g;
+                            o[x][y][1] *= g;
+                        }
                     }
                 }
-                ref_even = even;
-                ref_odd = odd;
             }
             const float ms = m == -INFINITY ? 0.f : m;
-            float p[4];
+            float p[4], most = 0.f;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 p[y] = ex2(s[y] - ms);
                 l += p[y];
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; y += 2)
+                    most = max3(most, p[y] * (power_of(sc[y].y, x) * c[x]), p[y + 1] * (power_of(sc[y + 1].y, x) * c[x]));
+            if (__any_sync(0xffffffffu, fresh || most > kTop)) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float g = 0.f;   // the row's largest product in the page
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) g = fmaxf(g, p[y] * power_of(sc[y].y, x));
+                    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+                    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+                    // c to 2^kLift over the power of two at or below it
+                    const uint32_t ex = __float_as_uint(g) >> 23;
+                    const float now = fminf(__uint_as_float((uint32_t)min(max(254 + kLift - (int)ex, 1), 254) << 23), kMostFactor);
+                    if (g < INFINITY && ((fresh && g > 0.f) || g * c[x] > kTop)) {
+                        const float h = now / c[x];
+                        c[x] = now;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            o[x][y][0] *= h;
+                            o[x][y][1] *= h;
+                        }
+                    }
+                }
             }
             // outputs: positions 2 kq, 2 kq + 1 (and + 8), dimensions 32 x + 4 n8 .. + 3 per lane
 #pragma unroll
@@ -308,8 +329,8 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
                 uint32_t wa[2], w[4];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const __half2 h = __floats2half2_rn(p[2 * y] * (power_of(sc[2 * y].y, x) * unscale[x]),
-                                                        p[2 * y + 1] * (power_of(sc[2 * y + 1].y, x) * unscale[x]));
+                    const __half2 h = __floats2half2_rn(p[2 * y] * (power_of(sc[2 * y].y, x) * c[x]),
+                                                        p[2 * y + 1] * (power_of(sc[2 * y + 1].y, x) * c[x]));
                     wa[y] = *reinterpret_cast<const uint32_t*>(&h);
                 }
 #pragma unroll
@@ -336,8 +357,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         if (valid) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int ref = (int)((x & 1 ? ref_odd : ref_even) >> (16 * (x >> 1)) & 255u);
-                const float f = inv * unit_of<kFmt>() * ex2((float)(ref - 127 - kLift));
+                const float f = inv * unit_of<kFmt>() / c[x];
                 float v[8];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {

@@ -1005,8 +1005,9 @@ ChunkLayout chunk_layout() {
 }
 
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream) {
-    // 8-bit caches and at most eight rows to a KV head and request on the average: 32 single tokens over 8K-164K positions
-    // take FEWROWS; either way every batch gives its result.
+    // 8-bit caches and at most eight rows to a KV head and request on the average: 32 single tokens of four heads to a group
+    // over 8K-164K positions of MXFP8 take 1.19 ms there and 1.67 ms here.  (Where one request has most of the rows after
+    // all, the result is the same and the tensor cores would have been faster.)
     if (format != kFmtBf16 && a.G <= 8 && (long)a.total_rows * a.G <= 8l * a.B) return launch_cache_decode(a, format, stream);
     return format == kFmtBf16 ? launch_format<kFmtBf16>(a, stream)
            : format == kFmtFp8 ? launch_format<kFmtFp8>(a, stream) : launch_format<kFmtInt8>(a, stream);

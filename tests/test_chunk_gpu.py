@@ -267,3 +267,25 @@ def test_workspace_shared_in_one_stream(fmt):
         for o, w, r in zip(outs, ws_, refs):
             ch.check_attention(o, w, r)
     assert all(int(d.status.item()) == 0 for d in ds)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "mxint8"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_large_values_under_small_weights(fmt, n):
+    """Positions whose V is 2^40 times the others' (and some 2^-90 times) but whose scores leave them nothing, at the
+    beginning, in between and at the end; and whole contexts of tiny and of huge values.  What a row weighs with 2^-60
+    must not cost the others their precision: its share of A is part of the bound."""
+    w = ch.Batch([n] * 4, [400, 70, 200, 333], 8, 2, fmt, seed=18)
+    w.q = torch.ones_like(w.q)
+    for b in range(4):
+        for p in range(w.total[b]):
+            pg, sl = int(w.page_table[b, p // 16]), p % 16
+            if b < 2:
+                w.src[0][pg, sl] = -8.0 if p % 37 in (0, 20, 36) else 0.0       # score -90 against 0
+                w.src[1][pg, sl] *= 2.0 ** (40 if p % 37 in (0, 36) else -90 if p % 37 == 20 else 0)
+            else:
+                w.src[1][pg, sl] *= 2.0 ** (-110 if b == 2 else 100)
+    w.encode()
+    d = w.gpu()
+    ch.check_attention(d.chunk(), w)
+    assert int(d.status.item()) == 0

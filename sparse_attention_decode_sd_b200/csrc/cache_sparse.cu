@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
             for (int z = 0; z < 2; ++z) {
                 float x = n8 < 2 ? o[0][y][z] : n8 < 4 ? o[1][y][z] : n8 < 6 ? o[2][y][z] : o[3][y][z];
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
-                v[4 * z + y] = M == -INFINITY ? 0.f : x * f;
+                v[4 * z + y] = x * f;   // (M = -infinity: 0, or NaN where every block was one)
             }
         const long slot = 2 * w + (j0 == 0 ? 1 : 0);   // a share's first row may have begun earlier; its last may go on
         float4* dst = reinterpret_cast<float4*>(whole ? a.out + (long)r * kHeadDim : part_out(a, slot)) + (n8 >> 1) * 8 + kq * 2;

@@ -259,3 +259,25 @@ def test_serving_over_an_8_bit_cache(fmt):
     sdb.sd_sparse_decode(shb, q, kb, vb, table, i32(total), idx, ref, sdb.workspace_for(shb, sdb.SD_OP_SPARSE, DEV), status)
     assert int(status.item()) == 0
     assert (out - ref).abs().max() <= 2e-4
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("which", [0, 1])
+def test_rows_that_read_as_nan(fmt, which):
+    """Block 2 of every selected row of one request reads as NaN, and of one row of another: K makes the whole output
+    NaN, V that block's; the third request is as ever."""
+    w = ch.Batch([1] * 3, [40, 50, 60], 4, 2, fmt, seed=22)
+    d = w.gpu()
+    idx = _select(w, [7, 20, 61], seed=22)
+    for b, rows in ((0, range(41)), (1, [int(idx[1, 0, 3])])):
+        for p in rows:
+            page, slot = int(w.page_table[b, p // 16]), p % 16
+            d.scales[page, :, slot, which, 2] = 255
+            (d.K, d.V)[which].view(torch.uint8)[page, slot, :, 64:96] = 0
+    out = _run(d, idx.to(DEV)).cpu()
+    assert int(d.status.item()) == 0
+    dims = slice(0, 128) if which == 0 else slice(64, 96)
+    assert out[0][:, dims].isnan().all() and out[1, 0, dims].isnan().all()
+    if which == 1:
+        assert out[:2, :, :64].isfinite().all() and out[:2, :, 96:].isfinite().all()
+    assert out[2].isfinite().all()

@@ -276,6 +276,8 @@ _CACHE_DTYPE = {SD_CACHE_BF16: torch.bfloat16, SD_CACHE_MXFP8: torch.float8_e4m3
 def make_cache(fmt: int, K, V, scales=None) -> SdCache:
     """Handle of a paged cache: K, V [num_pages][P][Hkv][d] of the format's element type and, for the 8-bit
     formats, scales uint8 [num_pages][Hkv][P][2][4].  It keeps the tensors alive."""
+    if any(t is not None and not t.is_contiguous() for t in (K, V, scales)):
+        raise ValueError("make_cache: the tensors must be contiguous")
     addr = [None if t is None else t.data_ptr() for t in (K, V, scales)]
     c = SdCache(int(fmt), 0, *addr)
     c.tensors = (K, V, scales)

@@ -156,3 +156,10 @@ def test_reference_attention_is_sdpa():
         o = torch.nn.functional.scaled_dot_product_attention(q, k, v, attn_mask=mask)
         got = torch.stack([ref[t][0] for t in range(w.start[b], w.start[b + 1])], 1)
         assert (got - o).abs().max() < 1e-12
+
+
+def test_make_cache_refuses_strided_tensors():
+    K = torch.zeros((2, 16, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="contiguous"):
+        sdb.make_cache(sdb.SD_CACHE_BF16, K.transpose(1, 2), K)
+    assert sdb.make_cache(sdb.SD_CACHE_BF16, K, K.clone()).tensors[0] is K

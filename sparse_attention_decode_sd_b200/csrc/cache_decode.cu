@@ -1,7 +1,7 @@
 // cache_decode.cu -- chunk attention of few rows per KV head over an 8-bit cache (single tokens, short drafts).
 //
-// The same result as chunk_attention.cu, for calls whose requests have about eight rows (tokens times the heads of a
-// group) or fewer.  There, a 128-row tile would be mostly empty, and expanding every 8-bit tile to bf16 in shared
+// The same result as chunk_attention.cu, for the requests of a batch that have at most eight rows (tokens times the heads
+// of a group).  There, a 128-row tile would be mostly empty, and expanding every 8-bit tile to bf16 in shared
 // memory moves three times the cache's bytes through it (96 KB written and read per 33 KB of cache: 3.3 TB/s of cache).
 // Here each warp streams pages on its own, one step per page: K, V (one TMA box of 16 rows x 128 bytes each, 128-byte
 // swizzle) and the page's 128 scale bytes into a ring of its own, and takes the elements from there straight into
@@ -12,8 +12,8 @@
 //            of V needs no scaling.  m is a running maximum of the scores that may lag by 2^8, and c_x a factor of the
 //            row and block that keeps the largest product so far near 2^6: half precision has few exponents, and where
 //            the largest scale stands beside a small weight it must not push the others out.
-// Weights enter as half precision (11 bits); their sum is fp32.  All steps of the batch are cut evenly over the warps of one wave; items cut by a border leave parts
-// in the workspace, which merge_decode_kernel joins in order.
+// Weights enter as half precision (11 bits); their sum is fp32.  All steps of the batch are cut evenly over the warps of
+// one wave; items cut by a border leave parts in the workspace, which merge_decode_kernel joins in order.
 //
 // What bounds it: instructions (about 580 per page of 16 positions; the schedulers issue 60% of the time with 12
 // warps per SM, and 16 warps spill registers: 1.51 ms instead of 1.19).  32 single tokens over 8K-164K positions, 32/8
@@ -30,6 +30,8 @@ namespace {
 constexpr int kRows = 8;                     // rows of an item
 constexpr int kRing = 4;                     // steps in a warp's ring
 constexpr int kCtasPerSm = 12;               // one warp each
+constexpr int kLeast = 8;                    // steps of a share on the average, in small calls (4: the same, 1: 10 us more,
+                                             // for the parts; 16: 5 us more)
 constexpr float kGrow = 8.f;                 // log2 units that the maximum may lag behind
 constexpr int kLift = 6;                     // log2 of what the largest weight is scaled to
 constexpr float kTop = 16384.f;              // weights from here on (half precision ends at 65504) rescale their row
@@ -57,7 +59,7 @@ __device__ __forceinline__ Req req_of(const ChunkArgs& a, int b) {
     r.n = a.row_start[b + 1] - r.rs;
     const int N = a.lens[b];
     r.base = N - r.n;
-    if (N < 0 || (long)N > a.n_cap || r.base < 0) r.n = 0;
+    if (N < 0 || (long)N > a.n_cap || r.base < 0 || r.n > a.few) r.n = 0;
     return r;
 }
 // Pages (steps) of item i: all positions that its last token sees.  tw tokens to an item.
@@ -65,8 +67,8 @@ __device__ __forceinline__ int item_steps(const Req& r, int i, int tw) {
     return (r.base + min(r.n, (i + 1) * tw) + kPageSize - 1) / kPageSize;
 }
 
-__device__ __forceinline__ float* part_of(const ChunkArgs& a, long slot) { return a.part + slot * (kRows * kHeadDim); }
-__device__ __forceinline__ float2* part_ml(const ChunkArgs& a, long slot) { return a.ml + slot * kRows; }
+__device__ __forceinline__ float* part_of(const ChunkArgs& a, long slot) { return a.few_part + slot * (kRows * kHeadDim); }
+__device__ __forceinline__ float2* part_ml(const ChunkArgs& a, long slot) { return a.few_ml + slot * kRows; }
 
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const void* tmap, int head, int row, uint64_t* bar) {
     asm volatile(
@@ -88,7 +90,8 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         mbar_fence_init();
     }
     __syncwarp();
-    pdl_enter();
+    pdl_wait();   // (first: chunk_attention_kernel may follow and not wait for this one, see there)
+    pdl_launch_dependents();
 
     // ---- the warp's share of all steps ----
     const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
@@ -101,13 +104,13 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
             if (blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
             continue;
         }
-        if (bad || hi == lo) continue;
+        if (bad || hi == lo || hi - lo > a.few) continue;
         const Req r = {lo, hi - lo, N - (hi - lo)};
         long steps = 0;
         for (int i = 0; i * tw < r.n; ++i) steps += item_steps(r, i, tw);
         mine += steps * a.Hkv;
     }
-    Tail* tail = reinterpret_cast<Tail*>(a.tail) + blockIdx.x;
+    Tail* tail = reinterpret_cast<Tail*>(a.few_tail) + blockIdx.x;
     if (lane == 0) *tail = Tail{};
     if (__any_sync(0xffffffffu, bad)) {
         if (lane == 0 && blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
@@ -120,7 +123,8 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         if (lane >= o) incl += t;
     }
     const long total = __shfl_sync(0xffffffffu, incl, 31);
-    const long shares = min(total, (long)gridDim.x), w = blockIdx.x;   // (each share has a step: no gaps between parts)
+    // (each share has a step: no gaps between parts)
+    const long shares = min((total + kLeast - 1) / kLeast, (long)gridDim.x), w = blockIdx.x;
     if (w >= shares) return;
     const long u0 = total * w / shares, u1 = total * (w + 1) / shares;
     int b = 0, kvh = 0, item = 0, step = 0;
@@ -398,32 +402,104 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
     }
 }
 
-// Joins the parts of the items that share borders cut: block c those of the item that began in share c, a thread per
-// row and four dimensions.
-__global__ void __launch_bounds__(kRows * 32) merge_decode_kernel(const __grid_constant__ ChunkArgs a) {
-    pdl_enter();
-    const Tail rec = reinterpret_cast<const Tail*>(a.tail)[blockIdx.x];
-    const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (!rec.valid || row >= rec.tokens * a.G) return;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int x = blockIdx.x; x <= rec.last; ++x) {   // slots: this share's second, then the first of each later one
-        const long slot = 2l * x + (x == (int)blockIdx.x ? 1 : 0);
-        const float2 ml = part_ml(a, slot)[row];
-        const float4 v = reinterpret_cast<const float4*>(part_of(a, slot) + row * kHeadDim)[lane];
-        const float top = fmaxf(m, ml.x), f = m == -INFINITY ? 0.f : ex2(m - top), g = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-        m = top;
-        l = fmaf(l, f, ml.y * g);
-        o.x = fmaf(o.x, f, v.x * g);
-        o.y = fmaf(o.y, f, v.y * g);
-        o.z = fmaf(o.z, f, v.z * g);
-        o.w = fmaf(o.w, f, v.w * g);
-    }
-    const float inv = 1.f / l;
-    const long dst = ((long)(rec.rows + row / a.G) * a.Hq + rec.kvh * a.G + row % a.G) * 32 + lane;
-    reinterpret_cast<uint2*>(a.out)[dst] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+// Joins the parts of the items that share borders cut: a block takes kCols columns (of four dimensions) of the items that
+// begin in its shares, one item at a time, with kGroups groups of threads that take every kGroups-th part, several loads
+// at once.
+constexpr int kAtOnce = 8;
+constexpr int kMine = 32;   // shares of a block at most 
+struct Sum {
+    float m, l;
+    float4 o;
+};
+__device__ __forceinline__ void add_part(Sum& s, float f, float l, const float4& v) {
+    s.l = fmaf(l, f, s.l);
+    s.o.x = fmaf(v.x, f, s.o.x);
+    s.o.y = fmaf(v.y, f, s.o.y);
+    s.o.z = fmaf(v.z, f, s.o.z);
+    s.o.w = fmaf(v.w, f, s.o.w);
 }
+__device__ __forceinline__ void raise(Sum& s, float m) {   // the reference to m, finite from the first part on that has a row
+    const float f = m > s.m ? ex2(s.m - m) : 1.f;
+    s.m = m;
+    s.l *= f;
+    s.o = make_float4(s.o.x * f, s.o.y * f, s.o.z * f, s.o.w * f);
+}
+template <int kGroups, int kCols>
+__global__ void __launch_bounds__(kGroups * kRows * kCols) merge_decode_kernel(const __grid_constant__ ChunkArgs a, int shares) {
+    __shared__ float4 sums[kGroups][kRows][kCols];
+    __shared__ float2 mls[kGroups][kRows];
+    pdl_wait();   // (first: as above, for merge_chunks_kernel)
+    pdl_launch_dependents();
+    const int group = threadIdx.x / (kRows * kCols), row = threadIdx.x / kCols % kRows, x8 = threadIdx.x % kCols;
+    const int col = blockIdx.y * kCols + x8;
+    // the block's tail records all at once
+    __shared__ Tail recs[kMine];
+    __shared__ int which[kMine], found;
+    if (threadIdx.x < 32) {
+        const int per = (shares + gridDim.x - 1) / gridDim.x, c = threadIdx.x < per ? blockIdx.x * per + threadIdx.x : shares;
+        Tail rec = {};
+        if (c < shares) rec = reinterpret_cast<const Tail*>(a.few_tail)[c];
+        const uint32_t live = __ballot_sync(0xffffffffu, rec.valid != 0);
+        if (rec.valid) {
+            const int at = __popc(live & ((1u << threadIdx.x) - 1u));
+            recs[at] = rec;
+            which[at] = c;
+        }
+        if (threadIdx.x == 0) found = __popc(live);
+    }
+    __syncthreads();
+    for (int i = 0; i < found; ++i) {
+        const Tail rec = recs[i];
+        const int c = which[i];
+        const bool on = row < rec.tokens * a.G;
+        Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (on) {
+            for (int x0 = c + group; x0 <= rec.last; x0 += kGroups * kAtOnce) {
+                float2 ml[kAtOnce];
+                float4 v[kAtOnce];
+                float m = s.m;
+#pragma unroll
+                for (int y = 0; y < kAtOnce; ++y) {
+                    const int x = x0 + y * kGroups;
+                    const long slot = 2l * x + (x == c ? 1 : 0);   // this share's second, then each later one's first
+                    ml[y] = make_float2(-INFINITY, 0.f);
+                    v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x <= rec.last) {
+                        ml[y] = part_ml(a, slot)[row];
+                        v[y] = reinterpret_cast<const float4*>(part_of(a, slot) + row * kHeadDim)[col];
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < kAtOnce; ++y) m = fmaxf(m, ml[y].x);
+                raise(s, m);
+                const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int y = 0; y < kAtOnce; ++y) add_part(s, ex2(ml[y].x - ms), ml[y].y, v[y]);
+            }
+            if (group > 0) {
+                sums[group][row][x8] = s.o;
+                if (x8 == 0) mls[group][row] = make_float2(s.m, s.l);
+            }
+        }
+        __syncthreads();
+        if (on && group == 0) {
+            float m = s.m;
+#pragma unroll
+            for (int x = 1; x < kGroups; ++x) m = fmaxf(m, mls[x][row].x);
+            raise(s, m);
+            const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int x = 1; x < kGroups; ++x) add_part(s, ex2(mls[x][row].x - ms), mls[x][row].y, sums[x][row][x8]);
+            const float inv = 1.f / s.l;
+            const long dst = ((long)(rec.rows + row / a.G) * a.Hq + rec.kvh * a.G + row % a.G) * 32 + col;
+            reinterpret_cast<uint2*>(a.out)[dst] =
+                make_uint2(pack_bf16x2(s.o.x * inv, s.o.y * inv), pack_bf16x2(s.o.z * inv, s.o.w * inv));
+        }
+        __syncthreads();
+    }
+}
+
+int decode_shares(const ChunkArgs& a) { return min(a.sms * kCtasPerSm, kDecodeShares); }
 
 template <int kFmt>
 cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
@@ -434,10 +510,8 @@ cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(cache_decode_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
-    const int ctas = min(a.sms * kCtasPerSm, kDecodeShares);
+    const int ctas = decode_shares(a);
     e = launch_pdl(cache_decode_kernel<kFmt>, dim3(ctas), dim3(32), sizeof(Smem), stream, a, km, vm);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(merge_decode_kernel, dim3(ctas), dim3(kRows * 32), 0, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -445,6 +519,18 @@ cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_decode(const ChunkArgs& a, int format, cudaStream_t stream) {
     return format == kFmtFp8 ? launch_format<kFmtFp8>(a, stream) : launch_format<kFmtInt8>(a, stream);
+}
+cudaError_t launch_merge_decode(const ChunkArgs& a, cudaStream_t stream) {
+    // Few items have many parts each (one token over 32768 positions and 8 KV heads: 222): eight groups and a quarter of
+    // the columns per block, 34 us for the whole call instead of 64 (eight tokens: 141 instead of 144; over 1024 positions 24
+    // instead of 21).  More items have few parts: a block per share (16 tokens over 300 positions: 22 us instead of 29).
+    const int shares = decode_shares(a);
+    const cudaError_t e =
+        (long)a.total_rows * a.Hkv <= 64
+            ? launch_pdl(merge_decode_kernel<8, 8>, dim3((shares + kMine / 2 - 1) / (kMine / 2), 4), dim3(8 * kRows * 8), 0,
+                         stream, a, shares)
+            : launch_pdl(merge_decode_kernel<1, 32>, dim3(shares), dim3(kRows * 32), 0, stream, a, shares);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace sd

@@ -139,7 +139,7 @@ __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
     r.n = a.row_start[b + 1] - r.rs;
     const int N = a.lens[b];
     r.base = N - r.n;
-    if (N < 0 || (long)N > a.n_cap || r.base < 0) r.n = 0;   // (reported where the shares are worked out)
+    if (N < 0 || (long)N > a.n_cap || r.base < 0 || r.n <= a.few) r.n = 0;   // (reported where the shares are worked out)
     return r;
 }
 
@@ -256,7 +256,7 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
             if (blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
             continue;
         }
-        if (bad || hi == lo) continue;
+        if (bad || hi - lo <= a.few) continue;
         last = Request{lo, hi - lo, N - (hi - lo)};
         const int items = (last.n + w - 1) / w;
         head = tiles_before(last, items, items, w);
@@ -865,6 +865,7 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qm,
                            const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
     using L = Layout<kFmt>;
+    constexpr bool k8 = L::k8;
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& c = *reinterpret_cast<Control*>(smem + L::kCtl);
     const int warp = threadIdx.x >> 5;
@@ -894,7 +895,8 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
         mbar_fence_init();
     }
     if (warp == 9) tmem_alloc(smem_addr(&c.tmem), 512);
-    pdl_enter();
+    pdl_launch_dependents();
+    if (!k8 || a.few == 0) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -915,6 +917,9 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 9) tmem_dealloc(c.tmem, 512);
+    // Behind cache_decode_kernel, which lets this kernel start only after its own wait for what came before: the two work
+    // side by side, and this one ends last.
+    if (k8 && a.few != 0) pdl_wait();
 }
 
 // Joins the parts of the items that CTA borders cut.  A warp takes 32 rows (a lane each) and four dimensions, so that its
@@ -925,7 +930,8 @@ static_assert(kMergeThreads >= kChunkCtas, "one thread per tail record");
 __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
     __shared__ TailRecord recs[kChunkCtas];
     __shared__ int before[kChunkCtas + 1], scratch[40];
-    pdl_enter();
+    pdl_launch_dependents();
+    if (a.few == 0) pdl_wait();   // (else behind merge_decode_kernel: as above)
     const int tid = threadIdx.x, lane = tid & 31, rows = a.tpt * a.G;
     int mine = 0, total;   // blocks of 32 rows
     if (tid < ctas) {
@@ -969,6 +975,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __gri
         reinterpret_cast<uint2*>(a.out)[dst] =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
+    if (a.few != 0) pdl_wait();
 }
 
 template <int kFmt>
@@ -985,6 +992,7 @@ cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
     const int ctas = a.sms < kChunkCtas ? a.sms : kChunkCtas;
     e = launch_pdl(chunk_attention_kernel<kFmt>, dim3(ctas), dim3(Layout<kFmt>::kThreads), chunk_smem<kFmt>(), stream, a, qm,
                    km, vm);
+    if (e == cudaSuccess && a.few != 0) e = launch_merge_decode(a, stream);
     if (e != cudaSuccess) return e;
     e = launch_pdl(merge_chunks_kernel, dim3(2 * ctas), dim3(kMergeThreads), 0, stream, a, ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -995,22 +1003,35 @@ cudaError_t launch_format(const ChunkArgs& a, cudaStream_t stream) {
 ChunkLayout chunk_layout() {
     ChunkLayout L;
     // two slots per CTA: of 256 rows here, of 8 rows in cache_decode.cu
-    const size_t slots = (size_t)2 * kChunkCtas * 2 * kTileRows, few = (size_t)2 * kDecodeShares * 8;
-    const size_t rows = slots > few ? slots : few;
+    const size_t rows = (size_t)2 * kChunkCtas * 2 * kTileRows, few = (size_t)2 * kDecodeShares * 8;
     L.part = 0;
     L.ml = rows * kHeadDim * sizeof(float);
     L.tail = L.ml + rows * sizeof(float2);
-    L.total = L.tail + (size_t)kDecodeShares * sizeof(TailRecord);
+    L.few_part = L.tail + kChunkCtas * sizeof(TailRecord);
+    L.few_ml = L.few_part + few * kHeadDim * sizeof(float);
+    L.few_tail = L.few_ml + few * sizeof(float2);
+    L.total = L.few_tail + kDecodeShares * sizeof(TailRecord);
     return L;
 }
 
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream) {
-    // 8-bit caches and at most eight rows to a KV head and request on the average: 32 single tokens of four heads to a group
-    // over 8K-164K positions of MXFP8 take 1.19 ms there and 1.67 ms here.  (Where one request has most of the rows after
-    // all, the result is the same and the tensor cores would have been faster.)
-    if (format != kFmtBf16 && a.G <= 8 && (long)a.total_rows * a.G <= 8l * a.B) return launch_cache_decode(a, format, stream);
-    return format == kFmtBf16 ? launch_format<kFmtBf16>(a, stream)
-           : format == kFmtFp8 ? launch_format<kFmtFp8>(a, stream) : launch_format<kFmtInt8>(a, stream);
+    // Requests over 8-bit caches with at most eight rows (tokens times heads of a group) go to cache_decode.cu: 32 single
+    // tokens of four heads to a group over 8K-164K positions of MXFP8 take 1.19 ms there and 1.67 ms here.  How many rows
+    // each request has is known on the device only, so both kernels look at the batch and each takes its requests: 31 tokens
+    // over 8K-64K positions with a chunk of 2048 rows take 0.80 ms, 1.50 ms with all of them here; a batch without work
+    // for one of the two pays 4 to 6 us for it.  Where there are no more rows than requests (single tokens, most often),
+    // all go there and nothing is launched here.
+    ChunkArgs rest = a;
+    rest.few = 0;
+    if (format != kFmtBf16 && a.G <= 8) {
+        const bool all = a.total_rows <= a.B;
+        rest.few = all ? 0x7fffffff : 8 / a.G;
+        const cudaError_t e = launch_cache_decode(rest, format, stream);
+        if (e != cudaSuccess) return e;
+        if (all) return launch_merge_decode(rest, stream);
+    }
+    return format == kFmtBf16 ? launch_format<kFmtBf16>(rest, stream)
+           : format == kFmtFp8 ? launch_format<kFmtFp8>(rest, stream) : launch_format<kFmtInt8>(rest, stream);
 }
 
 }  // namespace sd

@@ -189,20 +189,25 @@ struct ChunkArgs {
     float* part;              // un-normalised outputs
     float2* ml;               // maximum (log2 units) and sum of each row
     void* tail;               // per CTA: the item that goes on in later CTAs
+    float* few_part;          // the same for cache_decode.cu, two slots of eight rows per share
+    float2* few_ml;
+    void* few_tail;
     int B, Hq, Hkv, G, max_pages, num_pages, total_rows, sms;
     int tpt;                  // tokens to a tile of 128 rows: 128 / G
+    int few;                  // requests of at most so many new rows are cache_decode.cu's, the others chunk_attention.cu's
     long n_cap;
     float scale_log2;         // log2(e) / sqrt(d)
 };
 constexpr int kChunkCtas = 160;   // persistent CTAs at most
 struct ChunkLayout {
-    size_t part, ml, tail, total;
+    size_t part, ml, tail, few_part, few_ml, few_tail, total;
 };
 ChunkLayout chunk_layout();
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream);
 // The same for few rows per KV head over an 8-bit cache (cache_decode.cu).
 constexpr int kDecodeShares = 2048;   // warps of one wave at most
 cudaError_t launch_cache_decode(const ChunkArgs& a, int format, cudaStream_t stream);
+cudaError_t launch_merge_decode(const ChunkArgs& a, cudaStream_t stream);
 
 // Sparse decode over an 8-bit cache (cache_sparse.cu).
 struct CacheSparseArgs {

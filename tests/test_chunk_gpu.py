@@ -289,3 +289,29 @@ def test_large_values_under_small_weights(fmt, n):
     d = w.gpu()
     ch.check_attention(d.chunk(), w)
     assert int(d.status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (6, 2), (8, 1), (4, 4), (14, 2)])
+def test_tokens_prompts_and_drafts_in_one_call(fmt, Hq, Hkv):
+    """Single tokens, drafts of a few, a prompt and idle requests together: requests of few and of many rows take
+    different kernels of the call."""
+    n = [1, 1, 200, 2, 0, 1, 3, 1, 8, 9, 1, 0]
+    w = ch.Batch(n, [700, 0, 60, 33, 5, 2000, 150, 15, 90, 300, 127, 40], Hq, Hkv, fmt, seed=19, pad=3, lead=1)
+    d = w.gpu()
+    out = d.chunk()
+    assert int(d.status.item()) == 0
+    ch.check_attention(out, w)
+    assert (out[:1] == 7.0).all() and (out[w.T - 3:] == 7.0).all()   # rows of no request
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (7, 1)])
+def test_one_prompt_among_idle_requests(fmt, Hq, Hkv):
+    """No more rows than requests, but one request has nearly all of them."""
+    n = [0] * 60
+    n[7], n[30], n[59] = 1, 50, 2
+    w = ch.Batch(n, [(37 * b) % 300 for b in range(60)], Hq, Hkv, fmt, seed=20)
+    d = w.gpu()
+    ch.check_attention(d.chunk(), w)
+    assert int(d.status.item()) == 0

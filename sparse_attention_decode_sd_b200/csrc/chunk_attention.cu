@@ -526,6 +526,12 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
             qk(0, 0, k);
             qk(1, 1, k);
             commit(&c.kv_empty[k]);
+            auto q_done = [&](int t) {   // the stretch's last scores are under way: the next q may come
+                if (t + 1 < count) return;
+                commit(&c.q_empty[0]);
+                commit(&c.q_empty[1]);
+            };
+            q_done(0);
             for (int t = 0; t < count && ok; ++t) {
                 const uint32_t v = wait_stage();
                 const bool more = t + 1 < count;
@@ -538,16 +544,18 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
                     if (more) qk(g, g, k);
                     else commit(&c.o_full[g]);
                 }
-                if (more) commit(&c.kv_empty[k]);
+                if (more) {
+                    commit(&c.kv_empty[k]);
+                    q_done(t + 1);
+                }
             }
-            commit(&c.q_empty[0]);
-            commit(&c.q_empty[1]);
         } else {
             for (int g = 0; g < 2 && g < count; ++g) {
                 const uint32_t k = wait_stage();
                 qk(g, 0, k);
                 commit(&c.kv_empty[k]);
             }
+            if (count <= 2) commit(&c.q_empty[0]);
             for (int t = 0; t < count && ok; ++t) {
                 const int g = t & 1;
                 const uint32_t v = wait_stage();
@@ -558,11 +566,11 @@ __device__ __forceinline__ void mma_warp(const ChunkArgs& a, Control& c, uint8_t
                     const uint32_t k = wait_stage();
                     qk(g, 0, k);
                     commit(&c.kv_empty[k]);
+                    if (t + 3 == count) commit(&c.q_empty[0]);
                 } else {
                     commit(&c.o_full[g]);
                 }
             }
-            commit(&c.q_empty[0]);
         }
         if (!ok) break;
         stretches.done();
@@ -922,10 +930,11 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     if (k8 && a.few != 0) pdl_wait();
 }
 
-// Joins the parts of the items that CTA borders cut.  A warp takes 32 rows (a lane each) and four dimensions, so that its
-// reads of the parts are whole lines; every block reads all tail records at once and its warps take their work in
-// turn.  A short call then waits for few loads in a row.
-constexpr int kMergeThreads = 256;
+// Joins the parts of the items that CTA borders cut.  A warp takes 32 rows (a lane each) and 16 dimensions: its reads of the
+// parts are whole lines and its writes whole sectors (with four dimensions, a quarter of a sector, a prompt of 2048 rows
+// took 108 us in all instead of 80; two parts at once instead of four: 83).  Every block reads all tail records at once and
+// its warps take their work in turn.
+constexpr int kMergeThreads = 256, kChunks = 4, kPartsAtOnce = 4;
 static_assert(kMergeThreads >= kChunkCtas, "one thread per tail record");
 __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
     __shared__ TailRecord recs[kChunkCtas];
@@ -942,9 +951,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __gri
     if (tid < ctas) before[tid] = at;
     if (tid == 0) before[ctas] = total;
     __syncthreads();
-    total *= kHeadDim / 4;
+    constexpr int kPer = kHeadDim / 4 / kChunks;   // warps to a block of rows
+    total *= kPer;
     for (int w = blockIdx.x + gridDim.x * (tid >> 5); w < total; w += gridDim.x * (kMergeThreads / 32)) {
-        const int block = w / (kHeadDim / 4), chunk = w - block * (kHeadDim / 4);
+        const int block = w / kPer, chunk = (w - block * kPer) * kChunks;
         int c = 0, hi = ctas - 1;   // the last CTA with before <= block
         while (c < hi) {
             const int mid = (c + hi + 1) >> 1;
@@ -956,24 +966,50 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __gri
         if (k >= rec.tokens * a.G) continue;
         const int tile = k / rows, r = k - tile * rows, row = tile * kTileRows + r;
         float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int x = c; x <= rec.last; ++x) {   // slots: this CTA's second, then the first of each later CTA
-            const int slot = 2 * x + (x == c ? 1 : 0);
-            const float2 ml = slot_ml(a, slot)[row];
-            const float4 v = slot_out(a, slot, chunk)[row];
-            const float top = fmaxf(m, ml.x), f = m == -INFINITY ? 0.f : ex2(m - top), g = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+        float4 o[kChunks];
+#pragma unroll
+        for (int y = 0; y < kChunks; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x0 = c; x0 <= rec.last; x0 += kPartsAtOnce) {
+            float2 ml[kPartsAtOnce];
+            float4 v[kPartsAtOnce][kChunks];
+            float top = m;
+#pragma unroll
+            for (int z = 0; z < kPartsAtOnce; ++z) {
+                const int x = x0 + z, slot = 2 * x + (x == c ? 1 : 0);   // this CTA's second, then the first of each later CTA
+                ml[z] = make_float2(-INFINITY, 0.f);
+                if (x > rec.last) continue;
+                ml[z] = slot_ml(a, slot)[row];
+#pragma unroll
+                for (int y = 0; y < kChunks; ++y) v[z][y] = slot_out(a, slot, chunk + y)[row];
+            }
+#pragma unroll
+            for (int z = 0; z < kPartsAtOnce; ++z) top = fmaxf(top, ml[z].x);
+            const float f = m == -INFINITY ? 0.f : ex2(m - top);
             m = top;
-            l = fmaf(l, f, ml.y * g);
-            o.x = fmaf(o.x, f, v.x * g);
-            o.y = fmaf(o.y, f, v.y * g);
-            o.z = fmaf(o.z, f, v.z * g);
-            o.w = fmaf(o.w, f, v.w * g);
+            l *= f;
+#pragma unroll
+            for (int y = 0; y < kChunks; ++y) o[y] = make_float4(o[y].x * f, o[y].y * f, o[y].z * f, o[y].w * f);
+#pragma unroll
+            for (int z = 0; z < kPartsAtOnce; ++z) {
+                if (x0 + z > rec.last) continue;
+                const float g = ml[z].x == -INFINITY ? 0.f : ex2(ml[z].x - top);
+                l = fmaf(ml[z].y, g, l);
+#pragma unroll
+                for (int y = 0; y < kChunks; ++y) {
+                    o[y].x = fmaf(v[z][y].x, g, o[y].x);
+                    o[y].y = fmaf(v[z][y].y, g, o[y].y);
+                    o[y].z = fmaf(v[z][y].z, g, o[y].z);
+                    o[y].w = fmaf(v[z][y].w, g, o[y].w);
+                }
+            }
         }
         const float inv = 1.f / l;
-        const long dst = ((long)(rec.rows + tile * a.tpt + r / a.G) * a.Hq + rec.kvh * a.G + r % a.G) * 32 + chunk;
-        reinterpret_cast<uint2*>(a.out)[dst] =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        const long dst = (((long)(rec.rows + tile * a.tpt + r / a.G) * a.Hq + rec.kvh * a.G + r % a.G) * 32 + chunk) / 2;
+#pragma unroll
+        for (int y = 0; y < kChunks; y += 2)
+            reinterpret_cast<uint4*>(a.out)[dst + y / 2] =
+                make_uint4(pack_bf16x2(o[y].x * inv, o[y].y * inv), pack_bf16x2(o[y].z * inv, o[y].w * inv),
+                           pack_bf16x2(o[y + 1].x * inv, o[y + 1].y * inv), pack_bf16x2(o[y + 1].z * inv, o[y + 1].w * inv));
     }
     if (a.few != 0) pdl_wait();
 }

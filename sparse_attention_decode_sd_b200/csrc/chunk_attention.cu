@@ -6,8 +6,8 @@
 //
 // Rows of a tile.  The G query heads of a KV head read the same K and V, so a tile of 128 rows holds
 // floor(128 / G) consecutive tokens times the G heads of one group.  Two tiles make an item (256 rows, one KV
-// head of one request); its key/value tiles of 128 positions are the units of work, and all units of the
-// batch are cut evenly over one CTA per SM (each CTA works out its share from row_start and lens, so there
+// head of one request); its key/value tiles of 128 positions (and a few more for the item itself) are the units of work,
+// and all units of the batch are cut evenly over one CTA per SM (each CTA works out its share from row_start and lens, so there
 // is no planning launch).  An item cut by a CTA's border leaves its partial (max, sum, output) in the
 // workspace, and merge_chunks_kernel joins the parts in order: the same result every time.
 //
@@ -49,6 +49,10 @@ constexpr int kStageBytes = 2 * kHalf;         // a K or V tile in bf16
 constexpr int kRawBytes = 16 * 1024;           // the same in 8 bits
 constexpr int kScaleTile = 1024;               // scales of K and V of 128 positions
 constexpr int kExpandThreads = 256;            // that expand 8-bit tiles (half of them take twice as long: latency)
+// What an item costs besides its tiles, in tiles: its first reference, the wait for its last product, its output.  (About
+// 10000 cycles, 3300 to a tile.  Counted as 0, CTAs with many short items end last: prompts of 1000-4096 tokens 472 us
+// instead of 400, one of 8192 562 instead of 466; 2: 413 and 481; 4: 402 and 471.)
+constexpr int kItemCost = 3;
 constexpr float kFarAbove = 16384.f;            // sum of a tile's weights from which its row takes a new reference
 
 template <int kFmt>
@@ -143,27 +147,29 @@ __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
     return r;
 }
 
-// Key/value tiles of item i of a request: all positions that its last token sees.  w tokens to an item.
-__device__ __forceinline__ int item_tiles(const Request& r, int i, int w) {
-    return (r.base + min(r.n, (i + 1) * w) + kTileRows - 1) / kTileRows;
+// Units of item i of a request: a key/value tile each of the positions that its last token sees, behind kItemCost units
+// without a tile for what an item costs besides.  w tokens to an item.
+__device__ __forceinline__ int item_units(const Request& r, int i, int w) {
+    return kItemCost + (r.base + min(r.n, (i + 1) * w) + kTileRows - 1) / kTileRows;
 }
-// Tiles of items 0 .. i - 1.  Over p = 128 / gcd(w, 128) items their number grows by w p / 128 each, so the
+// Units of items 0 .. i - 1.  Over p = 128 / gcd(w, 128) items their number grows by w p / 128 each, so the
 // sum over whole periods has a closed form.
-__device__ __forceinline__ long long tiles_before(const Request& r, int i, int items, int w) {
+__device__ __forceinline__ long long units_before(const Request& r, int i, int items, int w) {
     const int k = min(i, items - 1);
     const int p = kTileRows / min(kTileRows, w & -w), s = w * p / kTileRows;
     const int whole = k / p, rest = k - whole * p;
     long long sum = 0, first = 0;
     if (whole > 0) {
-        for (int x = 0; x < p; ++x) first += item_tiles(r, x, w);
+        for (int x = 0; x < p; ++x) first += item_units(r, x, w);
         sum = whole * first + (long long)p * s * whole * (whole - 1) / 2;
     }
-    for (int x = 0; x < rest; ++x) sum += item_tiles(r, x, w) + (long long)whole * s;
-    if (i == items) sum += item_tiles(r, items - 1, w);
+    for (int x = 0; x < rest; ++x) sum += item_units(r, x, w) + (long long)whole * s;
+    if (i == items) sum += item_units(r, items - 1, w);
     return sum;
 }
 
-// CTAs that get units: each of them at least one, so that the parts of a cut item lie in neighbouring CTAs.
+// CTAs that get units: each of them at least one, so that the parts of a cut item lie in neighbouring CTAs (those that have
+// tiles of it: an item's units without a tile come first).
 __device__ __forceinline__ long long shares(long long total) { return min(total, (long long)gridDim.x); }
 
 // The first unit of CTA c's share.  (A 64-bit division costs hundreds of cycles, and the start of a short call counts.)
@@ -203,14 +209,15 @@ struct Walk {
         s.first = r.base + i * w;
         s.end = s.first + s.tokens;
         s.tiles = (s.end + kTileRows - 1) / kTileRows;
-        s.j0 = j;
-        s.j1 = (int)min((long long)s.tiles, j + left);
+        const int units = kItemCost + s.tiles, to = (int)min((long long)units, j + left);
+        s.j0 = max(0, j - kItemCost);
+        s.j1 = max(0, to - kItemCost);
         s.two = s.tokens > a.tpt ? 1 : 0;
-        left -= s.j1 - s.j0;
+        left -= to - j;
+        if (s.j1 == s.j0) return false;   // (the share ends before the item's first tile: the next one begins it)
         s.last = -1;
         if (left == 0 && s.j0 == 0 && s.j1 < s.tiles)
-            s.last = last_share(total, u1 - s.j1 + s.tiles);
-        j = s.j1;
+            s.last = last_share(total, u1 - to + units);
         if (left > 0) {   // the stretch ended with its item
             j = 0;
             if (++i == items) {
@@ -259,7 +266,7 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
         if (bad || hi - lo <= a.few) continue;
         last = Request{lo, hi - lo, N - (hi - lo)};
         const int items = (last.n + w - 1) / w;
-        head = tiles_before(last, items, items, w);
+        head = units_before(last, items, items, w);
         mine += a.Hkv * head;
     }
     if (__syncthreads_or(bad ? 1 : 0)) {
@@ -289,7 +296,7 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
             const Request r = per == 1 ? last : request(a, b);
             if (r.n == 0) continue;
             const int items = (r.n + w - 1) / w;
-            if (per > 1) head = tiles_before(r, items, items, w);
+            if (per > 1) head = units_before(r, items, items, w);
             if (at >= head * a.Hkv) {
                 at -= head * a.Hkv;
                 continue;
@@ -298,14 +305,14 @@ __device__ __forceinline__ bool plan(const ChunkArgs& a, Control& c, long long& 
             c.start = r;
             c.kvh = at < (1ll << 31) && head < (1ll << 31) ? (int)((uint32_t)at / (uint32_t)head) : (int)(at / head);
             at -= c.kvh * head;
-            int lo = 0, hi = items - 1;   // the last item with tiles_before <= at
+            int lo = 0, hi = items - 1;   // the last item with units_before <= at
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (tiles_before(r, mid, items, w) <= at) lo = mid;
+                if (units_before(r, mid, items, w) <= at) lo = mid;
                 else hi = mid - 1;
             }
             c.pair = lo;
-            c.unit = (int)(at - tiles_before(r, lo, items, w));
+            c.unit = (int)(at - units_before(r, lo, items, w));
             break;
         }
     }

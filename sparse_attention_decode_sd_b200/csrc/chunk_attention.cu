@@ -50,8 +50,8 @@ constexpr int kRawBytes = 16 * 1024;           // the same in 8 bits
 constexpr int kScaleTile = 1024;               // scales of K and V of 128 positions
 constexpr int kExpandThreads = 256;            // that expand 8-bit tiles (half of them take twice as long: latency)
 // What an item costs besides its tiles, in tiles: its first reference, the wait for its last product, its output.  (About
-// 10000 cycles, 3300 to a tile.  Counted as 0, CTAs with many short items end last: prompts of 1000-4096 tokens 472 us
-// instead of 400, one of 8192 562 instead of 466; 2: 413 and 481; 4: 402 and 471.)
+// 10000 cycles, 3300 to a tile.  Counted as 0, CTAs with many short items end last: prompts of 1000-4096 tokens
+// took 472 us instead of 400, one of 8192 562 instead of 466; 2: 413 and 481; 4: 402 and 471.)
 constexpr int kItemCost = 3;
 constexpr float kFarAbove = 16384.f;            // sum of a tile's weights from which its row takes a new reference
 
@@ -670,6 +670,22 @@ __device__ __forceinline__ void expand_warps(const ChunkArgs& a, Control& c, uin
 }
 
 // ---- warps 0-7: softmax and output --------------------------------------------------------------------------
+__device__ __forceinline__ void swap_if(uint4& lo, uint4& hi, int mask) {   // the lanes without the bit keep lo, the others hi
+    const bool up = threadIdx.x & mask;
+    const uint4 t = up ? lo : hi;
+    const uint4 r = make_uint4(__shfl_xor_sync(0xffffffffu, t.x, mask), __shfl_xor_sync(0xffffffffu, t.y, mask),
+                               __shfl_xor_sync(0xffffffffu, t.z, mask), __shfl_xor_sync(0xffffffffu, t.w, mask));
+    if (up) lo = r;
+    else hi = r;
+}
+// Lane i of four gets element i of each of their arrays, in the lanes' order.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
+    swap_if(v[0], v[1], 1);
+    swap_if(v[2], v[3], 1);
+    swap_if(v[0], v[2], 2);
+    swap_if(v[1], v[3], 2);
+}
+
 // kLook: blocks of 32 scores that are loaded together, and one such step ahead.  Two are faster (4096 tokens over
 // 65536 positions in bf16: 3.64 ms against 3.90), one fits the registers that the 8-bit caches' other warps leave.
 // kFma: of eight pairs of weights, those computed on the FMA pipe (with 8-bit caches it has other work too).
@@ -826,9 +842,13 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
         f0 *= inv;
         f1 *= inv;
         const uint32_t oa = s.two ? oc + g * 128 : oc;
+        const int own = valid ? (s.rows + token) * a.Hq + s.kvh * a.G + gi : -1;   // row of out (below 2^31)
+        int line[4];                                                                // those of the four lanes
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (!rows_here || x < from || x >= to) continue;
+        for (int y = 0; y < 4; ++y) line[y] = __shfl_sync(0xffffffffu, own, y, 4);
+#pragma unroll 1
+        for (int x = rows_here ? from : to; x < to; ++x) {   // (not unrolled: instructions used once per stretch
+                                                                 // are fetched anew; 4700 cycles unrolled, 3700 so)
             uint32_t o[32];
             tmem_ld32(oa + x * 32, o);
             tmem_wait_ld();
@@ -844,16 +864,20 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
                 for (int y = 0; y < 32; ++y)
                     o[y] = __float_as_uint(fmaf(__uint_as_float(o1[y]), f1, __uint_as_float(o[y])));
             }
-            if (valid && whole) {
-                uint4* dst = reinterpret_cast<uint4*>(a.out + ((long)(s.rows + token) * a.Hq + s.kvh * a.G + gi) * kHeadDim) + x * 4;
+            if (whole) {
+                uint4 v[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint32_t v[4];
+                for (int y = 0; y < 4; ++y)
+                    v[y] = make_uint4(pack_bf16x2(__uint_as_float(o[y * 8]), __uint_as_float(o[y * 8 + 1])),
+                                      pack_bf16x2(__uint_as_float(o[y * 8 + 2]), __uint_as_float(o[y * 8 + 3])),
+                                      pack_bf16x2(__uint_as_float(o[y * 8 + 4]), __uint_as_float(o[y * 8 + 5])),
+                                      pack_bf16x2(__uint_as_float(o[y * 8 + 6]), __uint_as_float(o[y * 8 + 7])));
+                // four lanes write 64 bytes of a row at a time (a lane its own row: 32 lines touched by each store)
+                transpose4(v);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        v[z] = pack_bf16x2(__uint_as_float(o[y * 8 + z * 2]), __uint_as_float(o[y * 8 + z * 2 + 1]));
-                    dst[y] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
+                for (int y = 0; y < 4; ++y)
+                    if (line[y] >= 0)
+                        reinterpret_cast<uint4*>(a.out)[(long)line[y] * 16 + x * 4 + (threadIdx.x & 3)] = v[y];
             } else if (valid) {
 #pragma unroll
                 for (int y = 0; y < 8; ++y)

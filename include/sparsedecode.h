@@ -322,7 +322,8 @@ SD_API sd_status sd_cache_read(const sd_shape* shape, const sd_cache* cache, con
  *   (q[row, h] . K[b, h/G, i]) / sqrt(d).
  *   q    bf16 [total_rows][Hq][d], device memory, 16-byte aligned.
  *   out  bf16 [total_rows][Hq][d], device memory, 16-byte aligned: rounded once, from fp32 sums.  The
- *        probabilities enter the second product as bf16 (their sum is taken before that, in fp32).
+ *        probabilities enter the second product as bf16, or as half precision for requests of at most eight rows
+ *        (tokens times Hq / Hkv) over an 8-bit cache; their sum is taken before that, in fp32.
  *   n_b > lens[b]: SD_ERR_INVALID_ARG and the request's rows are left as they were.  K and V of the positions
  *   below lens[b] must be finite (a position that a row may not see counts with weight 0, and 0 * inf is NaN);
  *   what the pages hold behind lens[b] does not matter.

@@ -20,6 +20,7 @@
 // heads: 1.19 ms in MXFP8 (5.6 GB, 4.7 TB/s), 1.44 ms in MXINT8, whose elements take one more instruction per pair.
 #include "cache_half.cuh"
 #include "kernels.h"
+#include "parts.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -407,23 +408,6 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
 // at once.
 constexpr int kAtOnce = 8;
 constexpr int kMine = 32;   // shares of a block at most 
-struct Sum {
-    float m, l;
-    float4 o;
-};
-__device__ __forceinline__ void add_part(Sum& s, float f, float l, const float4& v) {
-    s.l = fmaf(l, f, s.l);
-    s.o.x = fmaf(v.x, f, s.o.x);
-    s.o.y = fmaf(v.y, f, s.o.y);
-    s.o.z = fmaf(v.z, f, s.o.z);
-    s.o.w = fmaf(v.w, f, s.o.w);
-}
-__device__ __forceinline__ void raise(Sum& s, float m) {   // the reference to m, finite from the first part on that has a row
-    const float f = m > s.m ? ex2(s.m - m) : 1.f;
-    s.m = m;
-    s.l *= f;
-    s.o = make_float4(s.o.x * f, s.o.y * f, s.o.z * f, s.o.w * f);
-}
 template <int kGroups, int kCols>
 __global__ void __launch_bounds__(kGroups * kRows * kCols) merge_decode_kernel(const __grid_constant__ ChunkArgs a, int shares) {
     __shared__ float4 sums[kGroups][kRows][kCols];
@@ -452,12 +436,11 @@ __global__ void __launch_bounds__(kGroups * kRows * kCols) merge_decode_kernel(c
         const Tail rec = recs[i];
         const int c = which[i];
         const bool on = row < rec.tokens * a.G;
-        Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        PartSum s = no_parts();
         if (on) {
             for (int x0 = c + group; x0 <= rec.last; x0 += kGroups * kAtOnce) {
                 float2 ml[kAtOnce];
                 float4 v[kAtOnce];
-                float m = s.m;
 #pragma unroll
                 for (int y = 0; y < kAtOnce; ++y) {
                     const int x = x0 + y * kGroups;
@@ -469,12 +452,7 @@ __global__ void __launch_bounds__(kGroups * kRows * kCols) merge_decode_kernel(c
                         v[y] = reinterpret_cast<const float4*>(part_of(a, slot) + row * kHeadDim)[col];
                     }
                 }
-#pragma unroll
-                for (int y = 0; y < kAtOnce; ++y) m = fmaxf(m, ml[y].x);
-                raise(s, m);
-                const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int y = 0; y < kAtOnce; ++y) add_part(s, ex2(ml[y].x - ms), ml[y].y, v[y]);
+                join(s, ml, v);
             }
             if (group > 0) {
                 sums[group][row][x8] = s.o;
@@ -483,13 +461,16 @@ __global__ void __launch_bounds__(kGroups * kRows * kCols) merge_decode_kernel(c
         }
         __syncthreads();
         if (on && group == 0) {
-            float m = s.m;
+            float2 ml[kGroups];
+            float4 v[kGroups];
+            ml[0] = make_float2(-INFINITY, 0.f);
+            v[0] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int x = 1; x < kGroups; ++x) m = fmaxf(m, mls[x][row].x);
-            raise(s, m);
-            const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int x = 1; x < kGroups; ++x) add_part(s, ex2(mls[x][row].x - ms), mls[x][row].y, sums[x][row][x8]);
+            for (int x = 1; x < kGroups; ++x) {
+                ml[x] = mls[x][row];
+                v[x] = sums[x][row][x8];
+            }
+            join(s, ml, v);
             const float inv = 1.f / s.l;
             const long dst = ((long)(rec.rows + row / a.G) * a.Hq + rec.kvh * a.G + row % a.G) * 32 + col;
             reinterpret_cast<uint2*>(a.out)[dst] =

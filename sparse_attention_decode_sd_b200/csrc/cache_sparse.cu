@@ -27,6 +27,7 @@
 // the same number of rows is read in order; the whole call takes 64 us.
 #include "cache_half.cuh"
 #include "kernels.h"
+#include "parts.cuh"
 #include "tcgen05.cuh"
 
 namespace sd {
@@ -297,38 +298,57 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
     }
 }
 
-// Joins the parts of each row that a share's border cut; one warp per row, four dimensions per lane.
-constexpr int kJoinWarps = 4;
-__global__ void __launch_bounds__(kJoinWarps * 32) sparse_parts_kernel(const __grid_constant__ CacheSparseArgs a) {
+// Joins the parts of each row that a share's border cut: kSplit warps per row, each with every kSplit-th part, several at
+// once, and four dimensions per lane.
+constexpr int kFewParts = 16;   // parts of a row up to which one warp joins them (8 heads of 13107 entries, 192 parts: 38 us
+                                // for the call with one warp, 14 with 16; 4 parts: 13 us, 15 with 16 warps)
+constexpr int kJoinWarps = 4, kAtOnce = 8;
+template <int kSplit>
+__global__ void __launch_bounds__((kSplit > 1 ? kSplit : kJoinWarps) * 32)
+    sparse_parts_kernel(const __grid_constant__ CacheSparseArgs a) {
+    __shared__ float4 sums[kSplit][32];
+    __shared__ float2 mls[kSplit];
     pdl_enter();
-    const int lane = threadIdx.x & 31;
-    const long r = (long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5), rows = (long)a.B * a.Hq, W = a.shares;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, split = kSplit > 1 ? warp : 0;
+    const long r = kSplit > 1 ? blockIdx.x : (long)blockIdx.x * kJoinWarps + warp, rows = (long)a.B * a.Hq, W = a.shares;
     if (r >= rows) return;
     const long total = rows * a.k_max, begin = r * a.k_max, end = begin + a.k_max - 1;
     // the share that holds slot x: the w with total w / W <= x < total (w + 1) / W (rounded down)
     const long w0 = ((begin + 1) * W - 1) / total, w1 = ((end + 1) * W - 1) / total;
     if (w0 == w1) return;
-    auto slot_of = [&](long w) { return 2 * w + (w == w0 ? 1 : 0); };   // (the row begins in share w0)
-    float m = -INFINITY;
-    for (long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.ml[slot_of(w)].x);
+    PartSum s = no_parts();
+    for (long x0 = w0 + split; x0 <= w1; x0 += kSplit * kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 v[kAtOnce];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 8
-    for (long w = w0; w <= w1; ++w) {
-        const long slot = slot_of(w);
-        const float2 ml = a.ml[slot];
-        const float4 v = reinterpret_cast<const float4*>(part_out(a, slot))[lane];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        l = fmaf(ml.y, f, l);
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
+        for (int y = 0; y < kAtOnce; ++y) {
+            const long w = x0 + y * kSplit, slot = 2 * w + (w == w0 ? 1 : 0);   // (the row begins in share w0)
+            ml[y] = make_float2(-INFINITY, 0.f);
+            v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w <= w1) {
+                ml[y] = a.ml[slot];
+                v[y] = reinterpret_cast<const float4*>(part_out(a, slot))[lane];
+            }
+        }
+        join(s, ml, v);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<float4*>(a.out)[r * 32 + lane] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (kSplit > 1) {
+        sums[split][lane] = s.o;
+        if (lane == 0) mls[split] = make_float2(s.m, s.l);
+        __syncthreads();
+        if (split > 0) return;
+        float2 ml[kSplit];
+        float4 v[kSplit];
+#pragma unroll
+        for (int y = 0; y < kSplit; ++y) {
+            ml[y] = mls[y];
+            v[y] = sums[y][lane];
+        }
+        s = no_parts();
+        join(s, ml, v);
+    }
+    const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
+    reinterpret_cast<float4*>(a.out)[r * 32 + lane] = make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv);
 }
 
 template <int kFmt>
@@ -347,8 +367,10 @@ cudaError_t launch_format(CacheSparseArgs a, cudaStream_t stream) {
     e = launch_pdl(cache_sparse_kernel<kFmt>, dim3((unsigned)((shares + kWarps - 1) / kWarps)), dim3(kWarps * 32), kSmem, stream,
                    a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(sparse_parts_kernel, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, stream,
-                   a);
+    e = shares < kFewParts * rows
+            ? launch_pdl(sparse_parts_kernel<1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0,
+                         stream, a)
+            : launch_pdl(sparse_parts_kernel<16>, dim3((unsigned)rows), dim3(16 * 32), 0, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -281,3 +281,15 @@ def test_rows_that_read_as_nan(fmt, which):
     if which == 1:
         assert out[:2, :, :64].isfinite().all() and out[:2, :, 96:].isfinite().all()
     assert out[2].isfinite().all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,k", [(1, 1, 9000), (3, 1, 4000), (8, 2, 1500)])
+def test_few_rows_of_many_parts(Hq, Hkv, k):
+    """Few heads with many entries: every warp of the wave has a part of the same row."""
+    w = ch.Batch([1], [17999], Hq, Hkv, "mxfp8", seed=23)
+    idx = _select(w, [k], seed=23)
+    d = w.gpu()
+    out = _run(d, idx.to(DEV))
+    assert int(d.status.item()) == 0
+    _check(out, w, idx)
+    assert torch.equal(out, _run(d, idx.to(DEV)))

@@ -315,3 +315,47 @@ def test_one_prompt_among_idle_requests(fmt, Hq, Hkv):
     d = w.gpu()
     ch.check_attention(d.chunk(), w)
     assert int(d.status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_captured_call_over_changing_batches(fmt):
+    """One captured call replayed while the batch changes: which request has how many rows, and every length."""
+    batches = [ch.Batch(n, ctx, 8, 2, fmt, seed=24, spare=200)
+               for n, ctx in (([1, 1, 30, 2], [400, 20, 100, 33]), ([30, 1, 2, 1], [0, 500, 7, 64]), ([0, 0, 0, 34], [5, 16, 3, 300]),
+                              ([9, 8, 9, 8], [100, 128, 1, 90]))]
+    pages = max(w.max_pages for w in batches)
+    num = max(w.num_pages for w in batches)
+    shape = sdb.make_shape(4, 8, 2, pages, 1, num)
+    cache = sdb.empty_cache(shape, ch.FMTS[fmt], DEV)
+    q = torch.zeros((34, 8, 128), dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros((34, 8, 128), dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros((4, pages), dtype=torch.int32, device=DEV)
+    lens = torch.zeros(4, dtype=torch.int32, device=DEV)
+    start = torch.zeros(5, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = sdb.workspace_for(shape, sdb.SD_OP_CHUNK, DEV)
+
+    def load(w):
+        for t, x in zip(cache.tensors, (*w.kv, w.scales)):
+            if t is not None:
+                t[:w.num_pages].copy_(x)
+        table[:, :w.max_pages].copy_(w.page_table)
+        q.copy_(w.q)
+        lens.copy_(w.lens)
+        start.copy_(w.row_start)
+
+    def call():
+        sdb.sd_chunk_attention(shape, cache, q, table, lens, start, out, ws, status)
+
+    load(batches[0])
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for w in batches + batches[:1]:
+        load(w)
+        out.fill_(7.0)
+        g.replay()
+        ch.check_attention(out, w)
+        assert int(status.item()) == 0

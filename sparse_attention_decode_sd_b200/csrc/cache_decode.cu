@@ -31,8 +31,9 @@ namespace {
 constexpr int kRows = 8;                     // rows of an item
 constexpr int kRing = 4;                     // steps in a warp's ring
 constexpr int kCtasPerSm = 12;               // one warp each
-constexpr int kLeast = 8;                    // steps of a share on the average, in small calls (4: the same, 1: 10 us more,
-                                             // for the parts; 16: 5 us more)
+// Steps of a share on the average, in small calls (4: the same, 1: 10 us more, for the parts; 16: 5 us more), but no fewer
+// shares than items: a warp takes 3 us for each of them, however short (about 170 of one step each: 26 us instead of 53).
+constexpr int kLeast = 8;
 constexpr float kGrow = 8.f;                 // log2 units that the maximum may lag behind
 constexpr int kLift = 6;                     // log2 of what the largest weight is scaled to
 constexpr float kTop = 16384.f;              // weights from here on (half precision ends at 65504) rescale their row
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
     // ---- the warp's share of all steps ----
     const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
     bool bad = false;
-    long mine = 0;
+    long mine = 0, items = 0;
     for (int b = b0; b < b1; ++b) {
         const int lo = a.row_start[b], hi = a.row_start[b + 1], N = a.lens[b];
         bad = bad || lo < 0 || hi < lo || hi > a.total_rows;
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         long steps = 0;
         for (int i = 0; i * tw < r.n; ++i) steps += item_steps(r, i, tw);
         mine += steps * a.Hkv;
+        items += (long)((r.n + tw - 1) / tw) * a.Hkv;
     }
     Tail* tail = reinterpret_cast<Tail*>(a.few_tail) + blockIdx.x;
     if (lane == 0) *tail = Tail{};
@@ -124,8 +126,10 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         if (lane >= o) incl += t;
     }
     const long total = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
     // (each share has a step: no gaps between parts)
-    const long shares = min((total + kLeast - 1) / kLeast, (long)gridDim.x), w = blockIdx.x;
+    const long shares = min(max((total + kLeast - 1) / kLeast, items), (long)gridDim.x), w = blockIdx.x;
     if (w >= shares) return;
     const long u0 = total * w / shares, u1 = total * (w + 1) / shares;
     int b = 0, kvh = 0, item = 0, step = 0;

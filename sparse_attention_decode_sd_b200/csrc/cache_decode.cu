@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
                 l *= f;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {   // the products' references stay where they are, as far as c reaches
-                    const float now = fminf(c[x] / f, kMostFactor), g = now / c[x] * f;
+                    // (f is 0 behind a jump of more than 2^7: now * f / c is 0 then, where now / c may be infinite)
+                    const float now = fminf(c[x] / f, kMostFactor), g = now * f / c[x];
                     if (mt > -INFINITY && f != 1.f) {
                         c[x] = now;
 #pragma unroll

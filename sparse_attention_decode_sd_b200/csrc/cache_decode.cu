@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
             for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int y = 0; y < 4; y += 2)
-                    most = max3(most, p[y] * (power_of(sc[y].y, x) * c[x]), p[y + 1] * (power_of(sc[y + 1].y, x) * c[x]));
+                    most = max3(most, p[y] * c[x] * power_of(sc[y].y, x), p[y + 1] * c[x] * power_of(sc[y + 1].y, x));
             if (__any_sync(0xffffffffu, fresh || most > kTop)) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -333,14 +333,15 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
                     }
                 }
             }
-            // outputs: positions 2 kq, 2 kq + 1 (and + 8), dimensions 32 x + 4 n8 .. + 3 per lane
+            // outputs: positions 2 kq, 2 kq + 1 (and + 8), dimensions 32 x + 4 n8 .. + 3 per lane.  (Weight times factor first:
+            // that is finite, and 0 where the weight is; factor times scale may be infinite beside a weight of 0.)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t wa[2], w[4];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const __half2 h = __floats2half2_rn(p[2 * y] * (power_of(sc[2 * y].y, x) * c[x]),
-                                                        p[2 * y + 1] * (power_of(sc[2 * y + 1].y, x) * c[x]));
+                    const __half2 h = __floats2half2_rn(p[2 * y] * c[x] * power_of(sc[2 * y].y, x),
+                                                        p[2 * y + 1] * c[x] * power_of(sc[2 * y + 1].y, x));
                     wa[y] = *reinterpret_cast<const uint32_t*>(&h);
                 }
 #pragma unroll

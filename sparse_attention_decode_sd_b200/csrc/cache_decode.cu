@@ -37,7 +37,7 @@ constexpr int kLeast = 8;
 constexpr float kGrow = 8.f;                 // log2 units that the maximum may lag behind
 constexpr int kLift = 6;                     // log2 of what the largest weight is scaled to
 constexpr float kTop = 16384.f;              // weights from here on (half precision ends at 65504) rescale their row
-constexpr float kMostFactor = 1.2676506e30f; // 2^100: c_x at most
+constexpr float kMostFactor = 6.6461400e35f; // 2^119: c_x at most (times a weight of up to 2^kGrow it stays finite)
 
 struct Stage {
     uint8_t k[kPageSize][kHeadDim], v[kPageSize][kHeadDim];
@@ -364,16 +364,16 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         const bool whole = s0 == 0 && s1 == steps;
         const long slot = 2 * w + (s0 == 0 ? 1 : 0);
-        const float inv = whole ? 1.f / l : 1.f;
+        const float inv = (whole ? 1.f / l : 1.f) * unit_of<kFmt>();
         if (valid) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float f = inv * unit_of<kFmt>() / c[x];
+                const float f = 1.f / c[x];   // (not times inv first: that may fall below fp32's normal range)
                 float v[8];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    v[y] = o[x][y][0] * f;
-                    v[4 + y] = o[x][y][1] * f;
+                    v[y] = o[x][y][0] * inv * f;
+                    v[4 + y] = o[x][y][1] * inv * f;
                 }
                 if (whole) {
                     reinterpret_cast<uint4*>(a.out)[((row0 + tok) * a.Hq + kvh * a.G + head) * 16 + x * 4 + kq] =

@@ -88,3 +88,16 @@ def _huge_beside_small(fmt, n):
 @pytest.mark.parametrize("n", [1, 2])
 def test_huge_values_with_weight_zero_in_single_tokens_and_drafts(fmt, n):
     _huge_beside_small(fmt, n)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("n,power", [(1, -90), (1, -110), (1, -118), (2, -112), (40, -100)])
+def test_tiny_values(fmt, n, power):
+    w = ch.Batch([n] * 3, [70, 700, 1], 8, 2, fmt, seed=32)
+    for b in range(3):
+        for p in range(w.total[b]):
+            w.src[1][_place(w, b, p)] *= 2.0 ** power
+    w.encode()
+    d = w.gpu()
+    _check(d.chunk(), w)
+    assert int(d.status.item()) == 0

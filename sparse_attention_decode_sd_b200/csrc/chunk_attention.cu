@@ -26,10 +26,11 @@
 // addition, half a conversion.  Weights are exp2(s - m) for a reference m that need not be the running maximum, only
 // near it: a row takes its first tile's maximum, and a new one (with its sum and output rescaled, and the tile taken
 // again) when a tile's sum passes 2^14, which also catches infinities.  Sums and outputs are fp32 and bf16 has the
-// same precision at every magnitude, so nothing is lost.  Two of eight exponentials go to the FMA pipe (a cubic, 7.5e-5
-// relative, against 2^-9 for the rounding of the weights to bf16): the special-function unit alone would take
-// as long as the MMAs.  From scores to weights a tile of 128 x 128 takes 1580 cycles so, 500 more with a running maximum
-// and ex2 alone; with the wait for its products 3200, where the MMAs of the pair take 2048.
+// same precision at every magnitude, so nothing is lost.  All exponentials are the special-function unit's: a weight that
+// is 0 is exactly 0 and NaN stays NaN.  (A cubic on the FMA pipe for two of eight pairs took 381 us instead of 389 for
+// prompts of 1000-4096 tokens, 3.72 ms instead of 3.76 for a long chunk and the same over 8-bit caches, but has to be
+// clamped, so that what does not count weighed 2^-112; one more addition to take that off again costs what it gains.)  A tile of 128 x 128
+// takes about 3200 cycles with the wait for its products, where the MMAs of the pair take 2048.
 //
 // Items of one tile (few tokens: decode, short chunks) split their units between the two warpgroups, even and odd,
 // each with a maximum, sum and output of its own, joined at the end: the two sides stay busy in turn all the same.
@@ -689,8 +690,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
 
 // kLook: blocks of 32 scores that are loaded together, and one such step ahead.  Two are faster (4096 tokens over
 // 65536 positions in bf16: 3.64 ms against 3.90), one fits the registers that the 8-bit caches' other warps leave.
-// kFma: of eight pairs of weights, those computed on the FMA pipe (with 8-bit caches it has other work too).
-template <int kLook, int kFma>
+template <int kLook>
 __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
     const int cta = blockIdx.x;
     const int g = threadIdx.x >> 7, row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
@@ -756,7 +756,6 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
                 }
                 const float shift = m == -INFINITY ? 0.f : -m * scale;
                 const uint64_t sc2 = pair_of(scale, scale), sh2 = pair_of(shift, shift);
-                const float scu = scale / 128.f, shu = (shift + 112.f) / 128.f;
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int x = 0; x < kLook; ++x) tmem_ld32(sc + x * 32, r[x]);
@@ -779,18 +778,11 @@ __device__ __forceinline__ void softmax_warps(const ChunkArgs& a, Control& c) {
                     for (int y = 0; y < 16 * kLook; ++y) {   // pair y takes the place of values that were used before
                         const uint32_t(&src)[32] = r[h + (y >> 4)];
                         const int z = (y & 15) * 2;
-                        float lo = __uint_as_float(src[z]), hi = __uint_as_float(src[z + 1]);
-                        uint64_t e;
-                        if ((y & 7) < kFma) {
-                            e = ex2_fma2(pair_of(fma_sat(lo, scu, shu), fma_sat(hi, scu, shu)));
-                            split_pair(e, lo, hi);
-                        } else {
-                            split_pair(fma2(pair_of(lo, hi), sc2, sh2), lo, hi);
-                            lo = ex2(lo);
-                            hi = ex2(hi);
-                            e = pair_of(lo, hi);
-                        }
-                        sum[y & 1] = add2(sum[y & 1], e);
+                        float lo, hi;
+                        split_pair(fma2(pair_of(__uint_as_float(src[z]), __uint_as_float(src[z + 1])), sc2, sh2), lo, hi);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        sum[y & 1] = add2(sum[y & 1], pair_of(lo, hi));
                         r[h][y] = pack_bf16x2(lo, hi);
                     }
                 }
@@ -944,7 +936,7 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     plan(a, c, u0, u1, total);
     if (warp < 8) {
         regs_up<L::k8 ? 136 : 216>();
-        softmax_warps<L::k8 ? 1 : 2, L::k8 ? 1 : 2>(a, c);
+        softmax_warps<L::k8 ? 1 : 2>(a, c);
     } else if (warp < 12) {
         regs_down<L::k8 ? 64 : 72>();
         if (warp == 8 || warp == 10) copy_warps<kFmt>(a, c, smem, warp == 10, Walk(a, c, u0, u1, total), &qm, warp == 10 ? &vm : &km);

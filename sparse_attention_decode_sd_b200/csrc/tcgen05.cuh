@@ -147,29 +147,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// 2^x of two values on the FMA pipe, x = 128 u - 112 for u in [0, 1]: x = n + f with f in [-1/2, 1/2], 2^f by the polynomial
-// of degree 3 whose largest relative error is least (7.5e-5, from the exchange algorithm on 2^f), n added to the
-// exponent.  Adding 1.5 * 2^23 rounds to an integer and leaves it in the low bits.
-__device__ __forceinline__ uint64_t ex2_fma2(uint64_t u) {
-    const uint64_t span = pair_of(128.f, 128.f);
-    const uint64_t t = fma2(u, span, pair_of(12582912.f - 112.f, 12582912.f - 112.f));
-    const uint64_t n = fma2(t, pair_of(-1.f, -1.f), pair_of(12582912.f - 112.f, 12582912.f - 112.f));   // -(integer + 112)
-    const uint64_t f = fma2(u, span, n);
-    uint64_t p = pair_of(0.0551716685295105f, 0.0551716685295105f);
-    p = fma2(p, f, pair_of(0.2426111251115799f, 0.2426111251115799f));
-    p = fma2(p, f, pair_of(0.6932609677314758f, 0.6932609677314758f));
-    p = fma2(p, f, pair_of(0.9999280571937561f, 0.9999280571937561f));
-    float tl, th, pl, ph;
-    split_pair(t, tl, th);
-    split_pair(p, pl, ph);
-    return pair_of(__uint_as_float(__float_as_uint(pl) + (__float_as_uint(tl) << 23)),
-                   __uint_as_float(__float_as_uint(ph) + (__float_as_uint(th) << 23)));
-}
-__device__ __forceinline__ float fma_sat(float a, float b, float c) {
-    float r;
-    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

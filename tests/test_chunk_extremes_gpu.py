@@ -101,3 +101,36 @@ def test_tiny_values(fmt, n, power):
     d = w.gpu()
     _check(d.chunk(), w)
     assert int(d.status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt,n", [("bf16", 1), ("bf16", 2), ("bf16", 40), ("mxfp8", 40), ("mxint8", 40)])
+def test_huge_values_with_weight_zero_in_tiles(fmt, n):
+    _huge_beside_small(fmt, n)
+
+
+@pytest.mark.parametrize("fmt,n", [("bf16", 1), ("bf16", 2), ("bf16", 40), ("mxfp8", 40), ("mxint8", 40)])
+def test_huge_values_with_weight_zero_in_tiles(fmt, n):
+    _huge_beside_small(fmt, n)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "mxint8"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 1)])
+def test_a_query_that_is_not_finite_gives_nan(fmt, bad, Hq, Hkv):
+    """Its own row and head, wherever its positions fall in a tile; the others are not touched."""
+    w = ch.Batch([1, 1, 2, 40, 3], [0, 3, 1, 2, 700], Hq, Hkv, fmt, seed=33)
+    hurt = [(t, (3 * t + 1) % Hq) for t in range(w.T)]
+    for t, h in hurt:
+        w.q[t, h, (5 * t) % 128] = bad
+    d = w.gpu()
+    out = d.chunk()
+    assert int(d.status.item()) == 0
+    clean = torch.ones((w.T, Hq), dtype=torch.bool)
+    for t, h in hurt:
+        assert out[t, h].isnan().all(), (t, h)
+        clean[t, h] = False
+        w.q[t, h] = 0.0
+    out = out.double().cpu()
+    for t, (r, A) in w.attention().items():
+        ok = (out[t] - r).abs() <= 2.0 ** -8 * r.abs() + 1.25 * 2.0 ** -8 * A + 2.0 ** -134
+        assert ok[clean[t]].all(), t

@@ -92,8 +92,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
         mbar_fence_init();
     }
     __syncwarp();
-    pdl_wait();   // (first: chunk_attention_kernel may follow and not wait for this one, see there)
-    pdl_launch_dependents();
+    pdl_enter();
 
     // ---- the warp's share of all steps ----
     const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
@@ -418,8 +417,7 @@ template <int kGroups, int kCols>
 __global__ void __launch_bounds__(kGroups * kRows * kCols) merge_decode_kernel(const __grid_constant__ ChunkArgs a, int shares) {
     __shared__ float4 sums[kGroups][kRows][kCols];
     __shared__ float2 mls[kGroups][kRows];
-    pdl_wait();   // (first: as above, for merge_chunks_kernel)
-    pdl_launch_dependents();
+    pdl_enter();
     const int group = threadIdx.x / (kRows * kCols), row = threadIdx.x / kCols % kRows, x8 = threadIdx.x % kCols;
     const int col = blockIdx.y * kCols + x8;
     // the block's tail records all at once

@@ -897,7 +897,6 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qm,
                            const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
     using L = Layout<kFmt>;
-    constexpr bool k8 = L::k8;
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& c = *reinterpret_cast<Control*>(smem + L::kCtl);
     const int warp = threadIdx.x >> 5;
@@ -927,8 +926,7 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
         mbar_fence_init();
     }
     if (warp == 9) tmem_alloc(smem_addr(&c.tmem), 512);
-    pdl_launch_dependents();
-    if (!k8 || a.few == 0) pdl_wait();
+    pdl_enter();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -949,9 +947,6 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 9) tmem_dealloc(c.tmem, 512);
-    // Behind cache_decode_kernel, which lets this kernel start only after its own wait for what came before: the two work
-    // side by side, and this one ends last.
-    if (k8 && a.few != 0) pdl_wait();
 }
 
 // Joins the parts of the items that CTA borders cut.  A warp takes 32 rows (a lane each) and 16 dimensions: its reads of the
@@ -963,8 +958,7 @@ static_assert(kMergeThreads >= kChunkCtas, "one thread per tail record");
 __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __grid_constant__ ChunkArgs a, int ctas) {
     __shared__ TailRecord recs[kChunkCtas];
     __shared__ int before[kChunkCtas + 1], scratch[40];
-    pdl_launch_dependents();
-    if (a.few == 0) pdl_wait();   // (else behind merge_decode_kernel: as above)
+    pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, rows = a.tpt * a.G;
     int mine = 0, total;   // blocks of 32 rows
     if (tid < ctas) {
@@ -1035,7 +1029,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __gri
                 make_uint4(pack_bf16x2(o[y].x * inv, o[y].y * inv), pack_bf16x2(o[y].z * inv, o[y].w * inv),
                            pack_bf16x2(o[y + 1].x * inv, o[y + 1].y * inv), pack_bf16x2(o[y + 1].z * inv, o[y + 1].w * inv));
     }
-    if (a.few != 0) pdl_wait();
 }
 
 template <int kFmt>

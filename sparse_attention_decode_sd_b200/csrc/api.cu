@@ -733,6 +733,7 @@ sd_status sd_chunk_attention(const sd_shape* shape, const sd_cache* cache, const
     a.few_part = reinterpret_cast<float*>(ws + L.few_part);
     a.few_ml = reinterpret_cast<float2*>(ws + L.few_ml);
     a.few_tail = ws + L.few_tail;
+    a.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
     return launch_status(launch_chunk_attention(a, cache->format, static_cast<cudaStream_t>(stream)));
 }
 

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
 
     // ---- the warp's share of all steps ----
     const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
-    bool bad = false;
+    bool bad = false, more = false;
     long mine = 0, items = 0;
     for (int b = b0; b < b1; ++b) {
         const int lo = a.row_start[b], hi = a.row_start[b + 1], N = a.lens[b];
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
             if (blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
             continue;
         }
+        more = more || hi - lo > a.few;
         if (bad || hi == lo || hi - lo > a.few) continue;
         const Req r = {lo, hi - lo, N - (hi - lo)};
         long steps = 0;
@@ -114,7 +115,10 @@ __global__ void __launch_bounds__(32, kCtasPerSm)
     }
     Tail* tail = reinterpret_cast<Tail*>(a.few_tail) + blockIdx.x;
     if (lane == 0) *tail = Tail{};
-    if (__any_sync(0xffffffffu, bad)) {
+    bad = __any_sync(0xffffffffu, bad);
+    more = __any_sync(0xffffffffu, more);
+    if (lane == 0 && blockIdx.x == 0) *a.tiles = more && !bad;
+    if (bad) {
         if (lane == 0 && blockIdx.x == 0) report(a.status, SD_ERR_INVALID_ARG);
         return;
     }

@@ -931,8 +931,10 @@ __global__ void __launch_bounds__(Layout<kFmt>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     long long u0, u1, total;
-    plan(a, c, u0, u1, total);
-    if (warp < 8) {
+    const bool any = a.few == 0 || *a.tiles;   // (else every request is cache_decode.cu's)
+    if (any) plan(a, c, u0, u1, total);
+    if (!any) {
+    } else if (warp < 8) {
         regs_up<L::k8 ? 136 : 216>();
         softmax_warps<L::k8 ? 1 : 2>(a, c);
     } else if (warp < 12) {
@@ -960,6 +962,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const __gri
     __shared__ int before[kChunkCtas + 1], scratch[40];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, rows = a.tpt * a.G;
+    if (a.few != 0 && !*a.tiles) return;
     int mine = 0, total;   // blocks of 32 rows
     if (tid < ctas) {
         recs[tid] = reinterpret_cast<const TailRecord*>(a.tail)[tid];
@@ -1063,7 +1066,8 @@ ChunkLayout chunk_layout() {
     L.few_part = L.tail + kChunkCtas * sizeof(TailRecord);
     L.few_ml = L.few_part + few * kHeadDim * sizeof(float);
     L.few_tail = L.few_ml + few * sizeof(float2);
-    L.total = L.few_tail + kDecodeShares * sizeof(TailRecord);
+    L.tiles = L.few_tail + kDecodeShares * sizeof(TailRecord);
+    L.total = L.tiles + 256;
     return L;
 }
 
@@ -1071,14 +1075,19 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t 
     // Requests over 8-bit caches with at most eight rows (tokens times heads of a group) go to cache_decode.cu: 32 single
     // tokens of four heads to a group over 8K-164K positions of MXFP8 take 1.19 ms there and 1.67 ms here.  How many rows
     // each request has is known on the device only, so both kernels look at the batch and each takes its requests: 31 tokens
-    // over 8K-64K positions with a chunk of 2048 rows take 0.80 ms, 1.50 ms with all of them here; a batch without work
-    // for one of the two pays 4 to 6 us for it.  Where there are no more rows than requests (single tokens, most often),
-    // all go there and nothing is launched here.
+    // over 8K-64K positions with a chunk of 2048 rows take 0.79 ms, 1.50 ms with all of them here.  Where there is
+    // nothing for this kernel it learns so from one word: 32 tokens over 512 positions 30 us instead of 27, 256 over 4096
+    // 495 instead of 502.
+    // Calls of so few rows that this weighs more (8 tokens over 512 positions: 23 us instead of 31) go there whole: where no
+    // request can have more than eight rows, and up to four times as many where there are no more rows than requests (single
+    // tokens, most often).  If one request has them all, four items read its cache in turn: 8 tokens over 32768
+    // positions 82 us instead of 52, over 2048 25 instead of 30; with no such limit, 256 over 32768 took 1870 instead of 170.
     ChunkArgs rest = a;
     rest.few = 0;
     if (format != kFmtBf16 && a.G <= 8) {
-        const bool all = a.total_rows <= a.B;
-        rest.few = all ? 0x7fffffff : 8 / a.G;
+        const int few = 8 / a.G;
+        const bool all = a.total_rows <= few || (a.total_rows <= a.B && a.total_rows <= 4 * few);
+        rest.few = all ? 4 * few : few;
         const cudaError_t e = launch_cache_decode(rest, format, stream);
         if (e != cudaSuccess) return e;
         if (all) return launch_merge_decode(rest, stream);

@@ -192,6 +192,7 @@ struct ChunkArgs {
     float* few_part;          // the same for cache_decode.cu, two slots of eight rows per share
     float2* few_ml;
     void* few_tail;
+    int32_t* tiles;           // whether a request of this call is chunk_attention.cu's, where both take part
     int B, Hq, Hkv, G, max_pages, num_pages, total_rows, sms;
     int tpt;                  // tokens to a tile of 128 rows: 128 / G
     int few;                  // requests of at most so many new rows are cache_decode.cu's, the others chunk_attention.cu's
@@ -200,7 +201,7 @@ struct ChunkArgs {
 };
 constexpr int kChunkCtas = 160;   // persistent CTAs at most
 struct ChunkLayout {
-    size_t part, ml, tail, few_part, few_ml, few_tail, total;
+    size_t part, ml, tail, few_part, few_ml, few_tail, tiles, total;
 };
 ChunkLayout chunk_layout();
 cudaError_t launch_chunk_attention(const ChunkArgs& a, int format, cudaStream_t stream);

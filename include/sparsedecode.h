@@ -297,9 +297,12 @@ typedef struct sd_cache {
  * changed, so the same call may be repeated.
  *   k_new, v_new  bf16 [total_rows][Hkv][d], device memory, 16-byte aligned.
  *   boxes         NULL, or the Quest boxes (as for sd_quest_summarize; of the values as stored) to keep
- *                 current: the box of every page that gets a row becomes that of its rows, with the stored
- *                 box taken in where the page held earlier rows of the request.  A block that reads as NaN
- *                 leaves the other rows' bounds (NaN inputs are invalid to sd_quest_index).
+ *                 current: the box of every page that gets a row becomes that of all the request's rows in it, the
+ *                 new ones and those the cache holds in front of them, whatever the box was before (so rows that
+ *                 take the place of a rejected draft's leave nothing of it).  Boxes of other pages stay as they
+ *                 are; where only lens went down, the last page's is that of the longer context until a row is
+ *                 written to it.  A block that reads as NaN leaves the other rows' bounds (NaN inputs are invalid
+ *                 to sd_quest_index).
  * Two requests must not map new rows to the same page. */
 SD_API sd_status sd_cache_write(const sd_shape* shape, const sd_cache* cache, const int32_t* page_table,
                                 const int32_t* lens, const int32_t* row_start, int32_t total_rows, const void* k_new,

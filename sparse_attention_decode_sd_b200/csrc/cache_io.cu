@@ -11,7 +11,8 @@
 //
 // B200: 4 x 16384 rows x 8 heads from bf16 to MXFP8 with boxes 94 us (424 MB: 4.5 TB/s; one row per unit and a walk over the
 // page for its box took 383 us, two fp32 factors per value instead of one bf16 product 117 us); 131072 rows x 8 heads
-// of MXFP8 to bf16 139 us (814 MB: 5.8 TB/s); a decode step of 32 requests 8 us.
+// of MXFP8 to bf16 139 us (814 MB: 5.8 TB/s); a decode step of 32 requests with boxes 10 us
+// (8 without the read of each page's earlier rows for its box).
 #include "cache_half.cuh"
 #include "kernels.h"
 
@@ -24,6 +25,7 @@ constexpr int kIoCtas = 8;       // CTAs per SM at most (they take units in turn
 constexpr int kIoWave = 32;      // units per SM up to which runs are split
 constexpr int kWriteRows = 2;    // rows in flight per unit
 constexpr int kReadRows = 8;
+constexpr int kEarlierRows = 4;  // rows of a page that were there before, for its box
 
 // The last b with prefix[b] <= run.
 __device__ __forceinline__ int request_of(const int* prefix, int B, int run) {
@@ -65,6 +67,8 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& e, uint32_t byte) {
     decode4<kFmt>(e.y, f, r.z, r.w);
     return r;
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
 
 __device__ __forceinline__ void box_with(uint4& lo, uint4& hi, const uint4& v) {
     uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
@@ -154,9 +158,10 @@ __device__ __forceinline__ Run run_of(const CacheIoArgs& a, const int* prefix, i
     return u;
 }
 
-// New rows into the cache, and the Quest box of each run's page: the minimum and maximum, as stored, of its rows and
-// -- where the request had rows there before -- of the stored box.  Where runs are taken in parts, one more unit per run
-// makes the box alone (from the new rows, rounded again).
+// New rows into the cache, and the Quest box of each run's page: the minimum and maximum of its rows as stored, the new ones
+// and those that the request had there before.  (These are read again: the stored box may know rows that a rejected draft
+// had in the place of the new ones.  They lie before the new rows' slots, which alone are written here.)  Where runs
+// are taken in parts, one more unit per run makes the box alone (from the new rows, rounded again).
 template <int kFmt>
 __global__ void __launch_bounds__(kIoThreads, 4) cache_write_kernel(const __grid_constant__ CacheIoArgs a) {
     extern __shared__ int prefix[];
@@ -179,9 +184,13 @@ __global__ void __launch_bounds__(kIoThreads, 4) cache_write_kernel(const __grid
                                                           : reinterpret_cast<uint4*>(a.boxes) + ((long)u.page * a.Hkv + kvh) * 32 + c;
         uint4 lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);   // +inf, -inf
         uint4 hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-        if (box != nullptr && u.joins) {
-            lo = box[0];
-            hi = box[16];
+        const long page_row = ((long)u.page * kPageSize * a.Hkv + kvh) * 16;   // the page's first row, in chunks
+        const bool earlier = box != nullptr && u.joins;
+        if (earlier && c < u.slot) {   // a lane each of the request's earlier rows in the page, which are taken below
+            const uint8_t* row = static_cast<const uint8_t*>(a.K) + (page_row + c * step) * (kFmt == kFmtBf16 ? 16 : 8);
+            prefetch_l2(row);
+            if (kFmt == kFmtBf16) prefetch_l2(row + 128);
+            else prefetch_l2(a.scales + scale_offset(u.page, kvh, c, a.Hkv));
         }
         for (int j0 = 0; j0 < u.count; j0 += kWriteRows) {
             uint4 k[kWriteRows], v[kWriteRows];
@@ -217,6 +226,26 @@ __global__ void __launch_bounds__(kIoThreads, 4) cache_write_kernel(const __grid
                     if (box != nullptr) k[j] = dequantise8<kFmt>(ke, kb);
                 }
                 if (box != nullptr) box_with(lo, hi, k[j]);
+            }
+        }
+        if (earlier) {
+            const uint8_t* sc = kFmt == kFmtBf16 ? nullptr : a.scales + scale_offset(u.page, kvh, 0, a.Hkv) + (c >> 2);
+            for (int j0 = 0; j0 < u.slot; j0 += kEarlierRows) {
+                uint4 k[kEarlierRows];
+                uint2 e[kEarlierRows];
+                uint32_t by[kEarlierRows];
+#pragma unroll
+                for (int j = 0; j < kEarlierRows; ++j) {
+                    const int slot = min(j0 + j, u.slot - 1);   // (the last one again: no change to the box)
+                    if (kFmt == kFmtBf16) {
+                        k[j] = reinterpret_cast<const uint4*>(a.K)[page_row + c + slot * step];
+                    } else {
+                        e[j] = reinterpret_cast<const uint2*>(a.K)[page_row + c + slot * step];
+                        by[j] = sc[slot * 2 * kScaleBytes];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kEarlierRows; ++j) box_with(lo, hi, kFmt == kFmtBf16 ? k[j] : dequantise8<kFmt>(e[j], by[j]));
             }
         }
         if (box != nullptr) {

@@ -53,6 +53,7 @@ class SdShape(ctypes.Structure):
 class SdCache(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_int32), ("K", ctypes.c_void_p),
                 ("V", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+    pages = heads = None   # of the tensors behind it, where make_cache() made it
 
 
 class SdError(RuntimeError):
@@ -141,16 +142,12 @@ def shape_of(w) -> SdShape:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or type(t) is int else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:   # the current stream's handle, without making a Stream object for each call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -274,13 +271,28 @@ _CACHE_DTYPE = {SD_CACHE_BF16: torch.bfloat16, SD_CACHE_MXFP8: torch.float8_e4m3
 
 
 def make_cache(fmt: int, K, V, scales=None) -> SdCache:
-    """Handle of a paged cache: K, V [num_pages][P][Hkv][d] of the format's element type and, for the 8-bit
-    formats, scales uint8 [num_pages][Hkv][P][2][4].  It keeps the tensors alive."""
+    """Handle of a paged cache: K, V [num_pages][P][Hkv][d] of the format's element type (8-bit formats: or uint8) and, for
+    the 8-bit formats, scales uint8 [num_pages][Hkv][P][2][4].  It keeps the tensors alive."""
+    fmt = int(fmt)
+    if fmt not in _CACHE_DTYPE:
+        raise ValueError(f"make_cache: unknown format {fmt}")
     if any(t is not None and not t.is_contiguous() for t in (K, V, scales)):
         raise ValueError("make_cache: the tensors must be contiguous")
+    types = (_CACHE_DTYPE[fmt],) if fmt == SD_CACHE_BF16 else (_CACHE_DTYPE[fmt], torch.uint8)
+    if K.dtype not in types or V.dtype not in types:
+        raise ValueError(f"make_cache: K and V must be {types[0]}, not {K.dtype} and {V.dtype}")
+    if K.dim() != 4 or K.shape[1] != 16 or K.shape[3] != 128 or V.shape != K.shape:
+        raise ValueError(f"make_cache: K and V must be [num_pages][16][Hkv][128], not {list(K.shape)} and {list(V.shape)}")
+    if fmt != SD_CACHE_BF16:
+        want = (K.shape[0], K.shape[2], 16, 2, 4)
+        if scales is None or scales.dtype != torch.uint8 or tuple(scales.shape) != want:
+            raise ValueError(f"make_cache: scales must be uint8 {list(want)}")
+    if any(t is not None and t.device != K.device for t in (V, scales)):
+        raise ValueError("make_cache: the tensors must be on one device")
     addr = [None if t is None else t.data_ptr() for t in (K, V, scales)]
-    c = SdCache(int(fmt), 0, *addr)
+    c = SdCache(fmt, 0, *addr)
     c.tensors = (K, V, scales)
+    c.pages, c.heads = int(K.shape[0]), int(K.shape[2])
     return c
 
 
@@ -294,17 +306,61 @@ def empty_cache(shape: SdShape, fmt: int, device=None) -> SdCache:
     return make_cache(fmt, K, V, sc)
 
 
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def _cache_ok(what, shape, cache):
+    pages = cache.pages
+    if pages is not None and (pages < shape.num_pages or cache.heads != shape.num_kv_heads):
+        raise ValueError(f"{what}: a cache of {pages} pages and {cache.heads} KV heads for a shape of "
+                         f"{shape.num_pages} and {shape.num_kv_heads}")
+
+
+def _batch_ok(what, rows, heads, a, b, row_start, B):
+    """The arrays of a ragged batch, whose sizes sd_shape does not give: a, b bf16 [rows][heads][d] (or longer) on the current
+    device, row_start int32 [B + 1], all contiguous.  Addresses (int) are taken as they are.  One expression where all is
+    well: a call of a few rows takes hardly longer than this."""
+    n = rows * heads * 128
+    try:
+        if (a.dtype is _BF16 and b.dtype is _BF16 and a.is_contiguous() and b.is_contiguous() and a.numel() >= n
+                and b.numel() >= n and row_start.dtype is _I32 and row_start.is_contiguous() and row_start.numel() > B
+                and a.get_device() == torch._C._cuda_getDevice() == b.get_device()):
+            return
+    except (AttributeError, RuntimeError):   # an address; no device at all
+        pass
+    arrays = [t for t in (a, b) if not isinstance(t, int)]
+    for t in arrays:
+        if t.dtype is not _BF16 or not t.is_contiguous() or t.numel() < n:
+            raise ValueError(f"{what}: expected contiguous bf16 rows [{rows}][{heads}][128], got {t.dtype} {list(t.shape)}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+    _counts_ok(what, row_start, B + 1)
+    for t in arrays:
+        if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+            raise ValueError(f"{what}: the tensors must be on the current CUDA device, not on {t.device}")
+
+
+def _counts_ok(what, t, n):
+    if not isinstance(t, int) and (t.dtype is not _I32 or not t.is_contiguous() or t.numel() < n):
+        raise ValueError(f"{what}: expected contiguous int32 [{n}], got {t.dtype} {list(t.shape)}")
+
+
 def sd_cache_write(shape, cache, page_table, lens, row_start, k_new, v_new, boxes, dev_status, stream=None,
                    check=True) -> int:
+    rows = k_new.shape[0]
+    _cache_ok("sd_cache_write", shape, cache)
+    _batch_ok("sd_cache_write", rows, shape.num_kv_heads, k_new, v_new, row_start, shape.batch)
     st = load().sd_cache_write(ctypes.byref(shape), ctypes.byref(cache), _ptr(page_table), _ptr(lens), _ptr(row_start),
-                               int(k_new.shape[0]), _ptr(k_new), _ptr(v_new), _ptr(boxes), _ptr(dev_status),
-                               _stream(stream))
+                               rows, k_new.data_ptr(), _ptr(v_new), _ptr(boxes), _ptr(dev_status), _stream(stream))
     return _check(st, "sd_cache_write", check)
 
 
 def sd_cache_read(shape, cache, page_table, lens, first, row_start, k_out, v_out, dev_status, stream=None,
                   check=True) -> int:
-    rows = int((k_out if k_out is not None else v_out).shape[0])
+    a, b = (v_out if k_out is None else k_out), (k_out if v_out is None else v_out)
+    rows = a.shape[0]
+    _cache_ok("sd_cache_read", shape, cache)
+    _counts_ok("sd_cache_read", first, shape.batch)
+    _batch_ok("sd_cache_read", rows, shape.num_kv_heads, a, b, row_start, shape.batch)
     st = load().sd_cache_read(ctypes.byref(shape), ctypes.byref(cache), _ptr(page_table), _ptr(lens), _ptr(first),
                               _ptr(row_start), rows, _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream))
     return _check(st, "sd_cache_read", check)
@@ -312,14 +368,18 @@ def sd_cache_read(shape, cache, page_table, lens, first, row_start, k_out, v_out
 
 def sd_chunk_attention(shape, cache, q, page_table, lens, row_start, out, workspace, dev_status, stream=None,
                        check=True) -> int:
-    st = load().sd_chunk_attention(ctypes.byref(shape), ctypes.byref(cache), _ptr(q), _ptr(page_table), _ptr(lens),
-                                   _ptr(row_start), int(q.shape[0]), _ptr(out), _ptr(workspace), _ws_bytes(workspace),
+    rows = q.shape[0]
+    _cache_ok("sd_chunk_attention", shape, cache)
+    _batch_ok("sd_chunk_attention", rows, shape.num_q_heads, q, out, row_start, shape.batch)
+    st = load().sd_chunk_attention(ctypes.byref(shape), ctypes.byref(cache), q.data_ptr(), _ptr(page_table), _ptr(lens),
+                                   _ptr(row_start), rows, _ptr(out), _ptr(workspace), _ws_bytes(workspace),
                                    _ptr(dev_status), _stream(stream))
     return _check(st, "sd_chunk_attention", check)
 
 
 def sd_cache_sparse_decode(shape, cache, q, page_table, lens, idx, out, workspace, dev_status, stream=None,
                            check=True) -> int:
+    _cache_ok("sd_cache_sparse_decode", shape, cache)
     st = load().sd_cache_sparse_decode(ctypes.byref(shape), ctypes.byref(cache), _ptr(q), _ptr(page_table), _ptr(lens),
                                        _ptr(idx), _ptr(out), _ptr(workspace), _ws_bytes(workspace), _ptr(dev_status),
                                        _stream(stream))

@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         const bool whole = j0 == 0 && j1 == a.k_max;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-        const float f = M == -INFINITY ? 0.f : ex2(M - kLift - m) * inv;
+        // (in two factors where the block's scales are small: 2^(M - m) alone may lie below fp32's range)
+        const float d = M - kLift - m, off = d < 0.f ? 64.f : 0.f, back = d < 0.f ? 5.421010862427522e-20f : 1.f;   // 2^-64
+        const float f = M == -INFINITY ? 0.f : ex2(d + off) * inv;
         float v[8];   // dimensions 32 (n8 / 2) + 8 kq + 0 .. 7
 #pragma unroll
         for (int y = 0; y < 4; ++y)
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
             for (int z = 0; z < 2; ++z) {
                 float x = n8 < 2 ? o[0][y][z] : n8 < 4 ? o[1][y][z] : n8 < 6 ? o[2][y][z] : o[3][y][z];
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
-                v[4 * z + y] = x * f;   // (M = -infinity: 0, or NaN where every block was one)
+                v[4 * z + y] = x * f * back;   // (M = -infinity: 0, or NaN where every block was one)
             }
         const long slot = 2 * w + (j0 == 0 ? 1 : 0);   // a share's first row may have begun earlier; its last may go on
         float4* dst = reinterpret_cast<float4*>(whole ? a.out + (long)r * kHeadDim : part_out(a, slot)) + (n8 >> 1) * 8 + kq * 2;

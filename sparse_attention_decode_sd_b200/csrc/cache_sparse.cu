@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         const bool whole = j0 == 0 && j1 == a.k_max;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-        // (in two factors where the block's scales are small: 2^(M - m) alone may lie below fp32's range)
-        const float d = M - kLift - m, off = d < 0.f ? 64.f : 0.f, back = d < 0.f ? 5.421010862427522e-20f : 1.f;   // 2^-64
+        // (in two factors where the block's scales are tiny: 2^(M - m) alone may lie below fp32's range)
+        const float d = M - kLift - m, off = d < -64.f ? 64.f : 0.f, back = d < -64.f ? 5.421010862427522e-20f : 1.f;   // 2^-64
         const float f = M == -INFINITY ? 0.f : ex2(d + off) * inv;
         float v[8];   // dimensions 32 (n8 / 2) + 8 kq + 0 .. 7
 #pragma unroll

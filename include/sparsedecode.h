@@ -325,8 +325,13 @@ SD_API sd_status sd_cache_read(const sd_shape* shape, const sd_cache* cache, con
  *   (q[row, h] . K[b, h/G, i]) / sqrt(d).
  *   q    bf16 [total_rows][Hq][d], device memory, 16-byte aligned.
  *   out  bf16 [total_rows][Hq][d], device memory, 16-byte aligned: rounded once, from fp32 sums.  The
- *        probabilities enter the second product as bf16, or as half precision for requests of at most eight rows
- *        (tokens times Hq / Hkv) over an 8-bit cache; their sum is taken before that, in fp32.
+ *        probabilities enter the second product as bf16 (8 bits); their sum is taken before that, in fp32.
+ *        Requests of at most eight rows (tokens times Hq / Hkv; in calls of at most 32 such rows and no more tokens than
+ *        requests, all of them) over an 8-bit cache go another way, in half precision: q rounded to 11 bits or, where that
+ *        is coarser, to 2^-25 of its row's largest magnitude, and the products of probability and block scale to 11 bits
+ *        or to 2^-30 of the row's largest one in the block of 32 dimensions.
+ *   q    not finite: the row and head give NaN.  Sums of weight times V are fp32 before their division by the sum of
+ *        the weights: |V| times the number of positions has to stay below 2^119.
  *   n_b > lens[b]: SD_ERR_INVALID_ARG and the request's rows are left as they were.  K and V of the positions
  *   below lens[b] must be finite (a position that a row may not see counts with weight 0, and 0 * inf is NaN);
  *   what the pages hold behind lens[b] does not matter.
@@ -337,7 +342,8 @@ SD_API sd_status sd_chunk_attention(const sd_shape* shape, const sd_cache* cache
                                     int32_t* dev_status, void* stream);
 
 /* sd_sparse_decode over an 8-bit cache: the same selection format, checks, limits and fp32 result, over the
- * values the cache holds (SD_CACHE_BF16: SD_ERR_UNSUPPORTED, use sd_sparse_decode).  The Quest indexer reads
+ * values the cache holds (SD_CACHE_BF16: SD_ERR_UNSUPPORTED, use sd_sparse_decode).  q enters rounded to
+ * 11 bits or, where that is coarser, to 2^-25 of its row's largest magnitude, weights with 22 bits.  The Quest indexer reads
  * only boxes, so sd_cache_write with boxes, sd_quest_index and this call make a decode step without any bf16
  * cache.
  *   workspace  sd_workspace_size(shape, SD_OP_CACHE_SPARSE). */

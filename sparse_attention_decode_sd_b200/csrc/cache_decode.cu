@@ -1,7 +1,7 @@
 // cache_decode.cu -- chunk attention of few rows per KV head over an 8-bit cache (single tokens, short drafts).
 //
 // The same result as chunk_attention.cu, for the requests of a batch that have at most eight rows (tokens times the heads
-// of a group).  There, a 128-row tile would be mostly empty, and expanding every 8-bit tile to bf16 in shared
+// of a group; in small calls all of them, eight rows at a time).  There, a 128-row tile would be mostly empty, and expanding every 8-bit tile to bf16 in shared
 // memory moves three times the cache's bytes through it (96 KB written and read per 33 KB of cache: 3.3 TB/s of cache).
 // Here each warp streams pages on its own, one step per page: K, V (one TMA box of 16 rows x 128 bytes each, 128-byte
 // swizzle) and the page's 128 scale bytes into a ring of its own, and takes the elements from there straight into
@@ -11,7 +11,8 @@
 //   outputs  A = the weights, once for each block x: p_i 2^(e_x(i)) c_x with p_i = exp2(s_i - m), B = V, so that block x
 //            of V needs no scaling.  m is a running maximum of the scores that may lag by 2^8, and c_x a factor of the
 //            row and block that keeps the largest product so far near 2^6: half precision has few exponents, and where
-//            the largest scale stands beside a small weight it must not push the others out.
+//            the largest scale stands beside a small weight it must not push the others out.  c_x goes from 2^-126 to
+//            2^119, so that block scales of 2^-124 still give products of 2^-5.
 // Weights enter as half precision (11 bits); their sum is fp32.  All steps of the batch are cut evenly over the warps of
 // one wave; items cut by a border leave parts in the workspace, which merge_decode_kernel joins in order.
 //

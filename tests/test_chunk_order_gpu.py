@@ -64,3 +64,38 @@ def test_inputs_written_just_before(fmt):
 
     for a, b in zip(steps(lambda: None), steps(torch.cuda.synchronize)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+def test_batches_of_both_kinds_on_two_streams(fmt):
+    """Calls that launch both attention kernels, at once on two streams with a workspace each, eager and replayed."""
+    ws_ = [ch.Batch([1, 70, 1, 2], [900, 300, 2000, 17], 8, 2, fmt, seed=42), ch.Batch([40, 1, 3], [700, 2500, 60], 8, 2, fmt, seed=43)]
+    ds = [w.gpu() for w in ws_]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    work = [sdb.workspace_for(d.shape, sdb.SD_OP_CHUNK, DEV) for d in ds]
+    outs = [torch.full((w.T, w.Hq, 128), 7.0, dtype=torch.bfloat16, device=DEV) for w in ws_]
+    refs = [w.attention() for w in ws_]
+    graphs = []
+    for d, s, o, k in zip(ds, streams, outs, work):
+        d.chunk(out=o, ws=k)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            d.chunk(out=o, ws=k)
+        graphs.append(g)
+    for replay in (False, True):
+        for o, k in zip(outs, work):
+            o.fill_(7.0)
+            k.fill_(255)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for d, g, s, o, k in zip(ds, graphs, streams, outs, work):
+                with torch.cuda.stream(s):
+                    if replay:
+                        g.replay()
+                    else:
+                        d.chunk(out=o, ws=k)
+        torch.cuda.synchronize()
+        for w, d, o, r in zip(ws_, ds, outs, refs):
+            assert int(d.status.item()) == 0
+            ch.check_attention(o, w, r)

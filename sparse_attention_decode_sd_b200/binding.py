@@ -142,7 +142,7 @@ def shape_of(w) -> SdShape:
 
 
 def _ptr(t):
-    return t if t is None or type(t) is int else t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream):

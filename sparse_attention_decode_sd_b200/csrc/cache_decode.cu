@@ -1,8 +1,9 @@
 // cache_decode.cu -- chunk attention of few rows per KV head over an 8-bit cache (single tokens, short drafts).
 //
 // The same result as chunk_attention.cu, for the requests of a batch that have at most eight rows (tokens times the heads
-// of a group; in small calls all of them, eight rows at a time).  There, a 128-row tile would be mostly empty, and expanding every 8-bit tile to bf16 in shared
-// memory moves three times the cache's bytes through it (96 KB written and read per 33 KB of cache: 3.3 TB/s of cache).
+// of a group; in small calls for all of them, eight rows at a time).  There, a 128-row tile would be mostly empty, and
+// expanding every 8-bit tile to bf16 in shared memory moves three times the cache's bytes through it (96 KB written and
+// read per 33 KB of cache: 3.3 TB/s of cache).
 // Here each warp streams pages on its own, one step per page: K, V (one TMA box of 16 rows x 128 bytes each, 128-byte
 // swizzle) and the page's 128 scale bytes into a ring of its own, and takes the elements from there straight into
 // half-precision fragments, which hold them exactly (mma.sync m16n8k16, the eight rows in the upper half of A):

@@ -29,8 +29,8 @@
 // same precision at every magnitude, so nothing is lost.  All exponentials are the special-function unit's: a weight that
 // is 0 is exactly 0 and NaN stays NaN.  (A cubic on the FMA pipe for two of eight pairs took 381 us instead of 389 for
 // prompts of 1000-4096 tokens, 3.72 ms instead of 3.76 for a long chunk and the same over 8-bit caches, but has to be
-// clamped, so that what does not count weighed 2^-112; one more addition to take that off again costs what it gains.)  A tile of 128 x 128
-// takes about 3200 cycles with the wait for its products, where the MMAs of the pair take 2048.
+// clamped, so that what does not count weighed 2^-112; one more addition to take that off again costs what it gains.)  A
+// tile of 128 x 128 takes about 3200 cycles with the wait for its products, where the MMAs of the pair take 2048.
 //
 // Items of one tile (few tokens: decode, short chunks) split their units between the two warpgroups, even and odd,
 // each with a maximum, sum and output of its own, joined at the end: the two sides stay busy in turn all the same.

@@ -20,7 +20,10 @@
 //            the scale of block n folded in, B = V; of the result, block n of the output uses rows 2 n, 2 n + 1.
 //            Each block has a reference M_n of its own (near the largest s + e_n), as scales may span more than
 //            half precision's range; the sum of the weights has the reference m.
-// References lag by up to 2^8 before the accumulators are rescaled.
+// References lag by up to 2^8 before the accumulators are rescaled.  A step's products are added to the outputs by fp32
+// additions, which round to nearest: the tensor cores' own accumulation does not, and its errors, all towards zero, add up
+// over a share (root mean square error 1.2e-5 instead of 5.7e-7 over 590 steps, 3.9e-7 instead of 2.9e-7 over 24).  It
+// costs nothing at k = N/50 and 6% at k = N/2.
 //
 // What bounds it: random 128-byte rows.  At 4 x 64 heads x 2621 rows of N = 131072 (168 MB with each row of a group
 // read once) the gathers alone take 52 us for K and V, 4 us more for the scales' 32-byte sectors, and 27-40 us when
@@ -265,10 +268,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) cache_sparse_kernel(const 
                 }
                 const uint32_t e0 = __byte_perm(w[0], w[1], 0x5140), e1 = __byte_perm(w[0], w[1], 0x7362);
                 const uint32_t f0 = __byte_perm(w[2], w[3], 0x5140), f1 = __byte_perm(w[2], w[3], 0x7362);
-                mma_f16_upper(o[x][0], wa[0], wa[1], half_pair<kFmt, 0>(e0), half_pair<kFmt, 0>(f0));
-                mma_f16_upper(o[x][1], wa[0], wa[1], half_pair<kFmt, 1>(e0), half_pair<kFmt, 1>(f0));
-                mma_f16_upper(o[x][2], wa[0], wa[1], half_pair<kFmt, 0>(e1), half_pair<kFmt, 0>(f1));
-                mma_f16_upper(o[x][3], wa[0], wa[1], half_pair<kFmt, 1>(e1), half_pair<kFmt, 1>(f1));
+                float t[4][2] = {};
+                mma_f16_upper(t[0], wa[0], wa[1], half_pair<kFmt, 0>(e0), half_pair<kFmt, 0>(f0));
+                mma_f16_upper(t[1], wa[0], wa[1], half_pair<kFmt, 1>(e0), half_pair<kFmt, 1>(f0));
+                mma_f16_upper(t[2], wa[0], wa[1], half_pair<kFmt, 0>(e1), half_pair<kFmt, 0>(f1));
+                mma_f16_upper(t[3], wa[0], wa[1], half_pair<kFmt, 1>(e1), half_pair<kFmt, 1>(f1));
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    o[x][y][0] += t[y][0];
+                    o[x][y][1] += t[y][1];
+                }
             }
         }
         cp_async_wait<0>();
